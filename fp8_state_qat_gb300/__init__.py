@@ -1,4 +1,5 @@
-"""GB300 (sm_103a) chunked gated-delta-rule forward with dynamic FP8 E4M3 state/W QDQ.
+"""GB300 (sm_103a) chunked gated-delta-rule forward with dynamic FP8 E4M3 state/W QDQ, linear
+attention with a decay for each head, and the norms around both.
 
 The computation lives in the CUDA library ``libgdnqat.so`` (C ABI: include/gdnqat.h);
 this package is its ctypes binding plus the seeded synthetic-input generators.
@@ -28,4 +29,14 @@ from .gdnqat import (  # noqa: F401
     prefill_decode_workspace_bytes,
     status_string,
     workspace_bytes,
+)
+from .layer import (  # noqa: F401
+    gated_norm_bwd,
+    gated_norm_fwd,
+    la_chunk_bwd,
+    la_chunk_fwd,
+    la_chunk_workspace_bytes,
+    la_decode_step,
+    residual_norm_bwd,
+    residual_norm_fwd,
 )

@@ -138,4 +138,20 @@ struct BwdLayout {
 BwdLayout chunk_bwd_layout(const ChunkProblem& p);
 cudaError_t launch_chunk_bwd(const ChunkProblem& p, const BwdGrads& gr, void* ws, cudaStream_t stream);
 
+// ---- norms around a block (rows x D, contiguous; w fp32 or bf16, weight gradients fp32) ----
+bool norm_dim_ok(int D);                          // 1 .. 8192
+int64_t norm_bwd_parts(int64_t rows, int D);      // partial rows of a weight gradient (fp32 [parts][D] each)
+cudaError_t launch_gated_norm_fwd(const void* x, int x_f32, const void* z, const void* w, int w_bf16, void* y,
+                                  int64_t rows, int D, float eps, cudaStream_t stream);
+cudaError_t launch_gated_norm_bwd(const void* dy, const void* x, int x_f32, const void* z, const void* w, int w_bf16,
+                                  void* dx, void* dz, float* dw, int64_t rows, int D, float eps, float* part,
+                                  cudaStream_t stream);
+cudaError_t launch_residual_norm_fwd(const void* y, const void* h, int h_f32, const void* w_post, const void* w_pre,
+                                     int w_bf16, void* h_out, void* x, int64_t rows, int D, float alpha, float eps,
+                                     cudaStream_t stream);
+cudaError_t launch_residual_norm_bwd(const void* dx, const void* dh_out, const void* y, const void* h, int h_f32,
+                                     const void* w_post, const void* w_pre, int w_bf16, void* dy, void* dh,
+                                     float* dw_post, float* dw_pre, int64_t rows, int D, float alpha, float eps,
+                                     float* part, cudaStream_t stream);
+
 }  // namespace gdn

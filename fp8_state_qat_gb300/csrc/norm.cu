@@ -1,0 +1,516 @@
+// norm.cu -- RMS norms around a block, fused with the gate and the residual scale, and their gradients.
+//
+//   gated norm     y  = rms(x) w silu(z),                     rms(x) = x rsqrt(mean(x^2) + eps)
+//   residual norm  h' = h + alpha n,  n = rms(y) w_post (or y without w_post);  x = rms(h') w_pre
+//
+// A row is held by TPR threads, 8 elements each, from its load to its store, so every tensor moves
+// once: the kernels are bound by HBM (about 1 to 2 flops a byte). Statistics, sums and weight
+// gradients are fp32; each output is rounded once. VEC: element e of thread t is column 8 t + e and
+// moves in 16-byte accesses (D % 8 == 0, aligned pointers); otherwise column t + TPR e, one element
+// at a time, so that a warp still reads whole lines of a row of any length and alignment.
+// TPR is the power of two >= D / 8, at least 8: up to 32 threads a row reduces by shuffles alone and
+// a CTA holds 256 / TPR rows; above that a CTA holds one row (two for TPR 64, 128) and adds one
+// shared-memory step per reduction.
+//
+// The backward recomputes the statistics from the inputs it reads anyway (no tensor is saved for
+// it). Weight gradients are sums over all rows: each thread sums its columns over the rows its CTA
+// takes, a CTA adds its row groups in order, and a second launch adds the CTAs' partial rows in a
+// fixed order -- no atomics, the same bits every run.
+#include <initializer_list>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace gdn {
+namespace {
+
+constexpr int E = 8;                  // elements a thread
+
+__device__ __forceinline__ void load8f(const float* p, float* v) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float* v) { load_bf16x8(p, v); }
+__device__ __forceinline__ void store8f(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8f(__nv_bfloat16* p, const float* v) {
+  __nv_bfloat162 h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h);
+}
+__device__ __forceinline__ float tof(float x) { return x; }
+__device__ __forceinline__ float tof(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The 8 elements of thread t of a row; columns past D read as zero and are not written.
+template <int TPR, bool VEC, class T>
+__device__ __forceinline__ void load_row(const T* row, int D, int t, float* v) {
+  if (VEC) {
+    if (8 * t < D) load8f(row + 8 * t, v);
+    else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = t + TPR * e < D ? tof(row[t + TPR * e]) : 0.f;
+  }
+}
+template <int TPR, bool VEC, class T>
+__device__ __forceinline__ void store_row(T* row, int D, int t, const float* v) {
+  if (VEC) {
+    if (8 * t < D) store8f(row + 8 * t, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (t + TPR * e < D) put(row + t + TPR * e, v[e]);
+  }
+}
+// A weight of either type (bf16 or fp32), by a flag that is the same for the whole launch.
+template <int TPR, bool VEC>
+__device__ __forceinline__ void load_w(const void* w, int w_bf16, int D, int t, float* v) {
+  if (w_bf16) load_row<TPR, VEC>(static_cast<const __nv_bfloat16*>(w), D, t, v);
+  else load_row<TPR, VEC>(static_cast<const float*>(w), D, t, v);
+}
+
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+// Sums of M values over the TPR threads of a row, the same in each of them. `slot` alternates
+// between calls, so that one barrier a call is enough.
+template <int TPR, int M>
+struct RowSum {
+  static constexpr int kWarps = threads_of(TPR) / 32;
+  static __device__ __forceinline__ void run(float (&v)[M], float (*smem)[kWarps][2], int& slot) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
+    if (TPR > 32) {
+      const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+      if (lane == 0)
+#pragma unroll
+        for (int m = 0; m < M; ++m) smem[slot][warp][m] = v[m];
+      __syncthreads();
+      constexpr int PER = TPR / 32;         // warps a row
+      const int w0 = warp / PER * PER;
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        float s = lane < PER ? smem[slot][w0 + lane][m] : 0.f;
+#pragma unroll
+        for (int o = (PER < 32 ? PER : 32) / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        v[m] = __shfl_sync(0xffffffffu, s, 0);
+      }
+      slot ^= 1;
+    }
+  }
+};
+
+// silu(z) = z / (1 + exp(-z)) and its derivative; exp(-z) = inf gives 0 as it should
+__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + expf(-z)); }
+
+template <int TPR, bool VEC, class X>
+__global__ void __launch_bounds__(threads_of(TPR))
+gated_norm_fwd_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ z, const void* __restrict__ w,
+                      int w_bf16, __nv_bfloat16* __restrict__ y, int64_t rows, int D, float eps) {
+  constexpr int RPC = threads_of(TPR) / TPR;
+  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  int slot = 0;
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  float wv[E];
+  load_w<TPR, VEC>(w, w_bf16, D, t, wv);
+  const float inv_d = 1.f / (float)D;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
+    const int64_t r = r0 + rg;
+    const bool live = r < rows;
+    float xv[E] = {}, zv[E] = {};
+    if (live) {
+      load_row<TPR, VEC>(x + r * D, D, t, xv);
+      load_row<TPR, VEC>(z + r * D, D, t, zv);
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[0] = fmaf(xv[e], xv[e], s[0]);
+    RowSum<TPR, 1>::run(s, sm, slot);
+    const float rs = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    if (live) {
+      float o[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = xv[e] * rs * wv[e] * (zv[e] * sigmoidf(zv[e]));
+      store_row<TPR, VEC>(y + r * D, D, t, o);
+    }
+  }
+}
+
+// One row group's column sums of M weight gradients -> the CTA's partial row: the groups added in order.
+template <int TPR, bool VEC, int M>
+__device__ __forceinline__ void write_partials(float (&acc)[M][E], float* red, float* const (&out)[M], int D) {
+  constexpr int RPC = threads_of(TPR) / TPR;
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+#pragma unroll
+  for (int m = 0; m < M; ++m) {
+    if (!out[m]) continue;
+    if (RPC > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < E; ++e) red[(rg * E + e) * TPR + t] = acc[m][e];
+      __syncthreads();
+      if (rg == 0)
+        for (int g = 1; g < RPC; ++g)
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[m][e] += red[(g * E + e) * TPR + t];
+    }
+    if (rg == 0) store_row<TPR, VEC>(out[m] + (int64_t)blockIdx.x * D, D, t, acc[m]);
+  }
+}
+
+// With n = rms(x), s = silu(z), d = dy w s (the gradient at n):
+//   dx = r (d - n mean(d n)),  dz = dy n w silu'(z),  dw = sum over rows of dy n s
+template <int TPR, bool VEC, class X>
+__global__ void __launch_bounds__(threads_of(TPR))
+gated_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dy, const X* __restrict__ x,
+                      const __nv_bfloat16* __restrict__ z, const void* __restrict__ w, int w_bf16,
+                      X* __restrict__ dx, __nv_bfloat16* __restrict__ dz, float* __restrict__ part, int64_t rows,
+                      int D, float eps) {
+  constexpr int RPC = threads_of(TPR) / TPR;
+  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float red[RPC > 1 ? threads_of(TPR) * E : 1];
+  int slot = 0;
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  float wv[E], acc[1][E] = {};
+  load_w<TPR, VEC>(w, w_bf16, D, t, wv);
+  const float inv_d = 1.f / (float)D;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
+    const int64_t r = r0 + rg;
+    const bool live = r < rows;
+    float xv[E] = {}, zv[E] = {}, dv[E] = {};
+    if (live) {
+      load_row<TPR, VEC>(x + r * D, D, t, xv);
+      load_row<TPR, VEC>(z + r * D, D, t, zv);
+      load_row<TPR, VEC>(dy + r * D, D, t, dv);
+    }
+    float s[2] = {0.f, 0.f}, sg[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      sg[e] = sigmoidf(zv[e]);
+      s[0] = fmaf(xv[e], xv[e], s[0]);
+      s[1] = fmaf(dv[e] * wv[e] * (zv[e] * sg[e]), xv[e], s[1]);
+    }
+    RowSum<TPR, 2>::run(s, sm, slot);
+    const float rs = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float c = s[1] * inv_d * rs * rs;      // mean(d n) r, the factor of x in n mean(d n)
+    if (live) {
+      float ox[E], oz[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float si = zv[e] * sg[e], n = xv[e] * rs, dn = dv[e] * n;
+        ox[e] = rs * fmaf(-c, xv[e], dv[e] * wv[e] * si);
+        oz[e] = dn * wv[e] * (sg[e] * (1.f + zv[e] * (1.f - sg[e])));
+        acc[0][e] = fmaf(dn, si, acc[0][e]);
+      }
+      store_row<TPR, VEC>(dx + r * D, D, t, ox);
+      store_row<TPR, VEC>(dz + r * D, D, t, oz);
+    }
+  }
+  float* const out[1] = {part};
+  write_partials<TPR, VEC, 1>(acc, red, out, D);
+}
+
+template <int TPR, bool VEC, bool POST, class H>
+__global__ void __launch_bounds__(threads_of(TPR))
+residual_norm_fwd_kernel(const __nv_bfloat16* __restrict__ y, const H* h, const void* __restrict__ w_post,
+                         const void* __restrict__ w_pre, int w_bf16, H* h_out,
+                         __nv_bfloat16* __restrict__ x, int64_t rows, int D, float alpha, float eps) {
+  constexpr int RPC = threads_of(TPR) / TPR;
+  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  int slot = 0;
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  float w1[E], w2[E];
+  load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
+  if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
+  const float inv_d = 1.f / (float)D;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
+    const int64_t r = r0 + rg;
+    const bool live = r < rows;
+    float yv[E] = {}, hv[E] = {};
+    if (live) {
+      load_row<TPR, VEC>(y + r * D, D, t, yv);
+      load_row<TPR, VEC>(h + r * D, D, t, hv);
+    }
+    float ry = 1.f;
+    if (POST) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
+      RowSum<TPR, 1>::run(s, sm, slot);
+      ry = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    }
+    float s[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      hv[e] = fmaf(alpha, POST ? yv[e] * ry * w2[e] : yv[e], hv[e]);
+      s[0] = fmaf(hv[e], hv[e], s[0]);
+    }
+    RowSum<TPR, 1>::run(s, sm, slot);
+    const float rh = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    if (live) {
+      store_row<TPR, VEC>(h_out + r * D, D, t, hv);
+#pragma unroll
+      for (int e = 0; e < E; ++e) yv[e] = hv[e] * rh * w1[e];
+      store_row<TPR, VEC>(x + r * D, D, t, yv);
+    }
+  }
+}
+
+// With m = rms(h'), n = rms(y) (POST), p = dx w_pre:
+//   dh = dh' + r_h (p - m mean(p m)),  e = alpha dh,  dw_pre = sum dx m
+//   POST: dy = r_y (e w_post - n mean(e w_post n)), dw_post = sum e n;  else dy = e
+template <int TPR, bool VEC, bool POST, class H>
+__global__ void __launch_bounds__(threads_of(TPR))
+residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
+                         const __nv_bfloat16* __restrict__ y, const H* __restrict__ h, const void* __restrict__ w_post,
+                         const void* __restrict__ w_pre, int w_bf16, __nv_bfloat16* __restrict__ dy,
+                         H* dh, float* __restrict__ part_pre, float* __restrict__ part_post, int64_t rows,
+                         int D, float alpha, float eps) {
+  constexpr int RPC = threads_of(TPR) / TPR;
+  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float red[RPC > 1 ? threads_of(TPR) * E : 1];
+  int slot = 0;
+  const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  float w1[E], w2[E], acc[2][E] = {};
+  load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
+  if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
+  const float inv_d = 1.f / (float)D;
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
+    const int64_t r = r0 + rg;
+    const bool live = r < rows;
+    float yv[E] = {}, hv[E] = {}, dv[E] = {}, dhv[E] = {};
+    if (live) {
+      load_row<TPR, VEC>(y + r * D, D, t, yv);
+      load_row<TPR, VEC>(h + r * D, D, t, hv);
+      load_row<TPR, VEC>(dx + r * D, D, t, dv);
+      if (dh_out) load_row<TPR, VEC>(dh_out + r * D, D, t, dhv);
+    }
+    float ry = 1.f;
+    if (POST) {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
+      RowSum<TPR, 1>::run(s, sm, slot);
+      ry = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    }
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      hv[e] = fmaf(alpha, POST ? yv[e] * ry * w2[e] : yv[e], hv[e]);
+      s[0] = fmaf(hv[e], hv[e], s[0]);
+      s[1] = fmaf(dv[e] * w1[e], hv[e], s[1]);
+    }
+    RowSum<TPR, 2>::run(s, sm, slot);
+    const float rh = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float c = s[1] * inv_d * rh * rh;
+    float q[1] = {0.f};
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      acc[0][e] = fmaf(dv[e], hv[e] * rh, acc[0][e]);
+      dhv[e] += rh * fmaf(-c, hv[e], dv[e] * w1[e]);
+      if (POST) q[0] = fmaf(alpha * dhv[e] * w2[e], yv[e], q[0]);
+    }
+    if (live) store_row<TPR, VEC>(dh + r * D, D, t, dhv);
+    if (POST) {
+      RowSum<TPR, 1>::run(q, sm, slot);
+      const float cy = q[0] * inv_d * ry * ry;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const float en = alpha * dhv[e];
+        acc[1][e] = fmaf(en, yv[e] * ry, acc[1][e]);
+        yv[e] = ry * fmaf(-cy, yv[e], en * w2[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) yv[e] = alpha * dhv[e];
+    }
+    if (live) store_row<TPR, VEC>(dy + r * D, D, t, yv);
+  }
+  float* const out[2] = {part_pre, POST ? part_post : nullptr};
+  write_partials<TPR, VEC, 2>(acc, red, out, D);
+}
+
+// out[m][d] = the sum of the m-th array's `parts` partial rows, in a fixed order: 8 lanes of rows per
+// column, each summing every 8th row, added by an xor tree.
+__global__ void __launch_bounds__(256) sum_partials_kernel(const float* __restrict__ p0, const float* __restrict__ p1,
+                                                           float* __restrict__ o0, float* __restrict__ o1, int parts,
+                                                           int D) {
+  const float* p = blockIdx.y ? p1 : p0;
+  float* o = blockIdx.y ? o1 : o0;
+  const int cl = threadIdx.x & 7, pl = threadIdx.x >> 3;   // 8 columns x 32 row lanes
+  const int d = blockIdx.x * 8 + cl;
+  float s = 0.f;
+  if (d < D)
+    for (int i = pl; i < parts; i += 32) s += p[(int64_t)i * D + d];
+  __shared__ float red[32][9];
+  red[pl][cl] = s;
+  __syncthreads();
+  if (threadIdx.x < 8 && d < D) {
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 32; ++i) a[i & 3] += red[i][threadIdx.x];
+    o[d] = (a[0] + a[1]) + (a[2] + a[3]);
+  }
+}
+
+constexpr int kSMs = 152;
+constexpr int kMaxD = 8192;
+
+int tpr_of(int D) {
+  int t = 8;
+  while (t * E < D) t *= 2;
+  return t;
+}
+// CTAs of a launch: enough for every row group, at most `per_sm` resident ones per SM.
+int64_t grid_of(int64_t rows, int tpr, int per_sm) {
+  const int64_t rpc = threads_of(tpr) / tpr;
+  const int64_t need = (rows + rpc - 1) / rpc, most = (int64_t)kSMs * per_sm;
+  return need < most ? need : most;
+}
+// 64-register kernels: 1024 threads an SM in flight
+int per_sm_of(int tpr) { return 1024 / threads_of(tpr); }
+
+bool vec_ok(int D, std::initializer_list<const void*> ptrs) {
+  if (D % 8) return false;
+  for (const void* p : ptrs)
+    if (reinterpret_cast<uintptr_t>(p) & 15) return false;
+  return true;
+}
+
+// Calls f(tpr, vec) with both as compile-time constants.
+template <class F>
+void dispatch(int tpr, bool vec, F f) {
+  auto go = [&](auto t) {
+    if (vec) f(t, std::true_type());
+    else f(t, std::false_type());
+  };
+  switch (tpr) {
+    case 8: go(std::integral_constant<int, 8>()); break;
+    case 16: go(std::integral_constant<int, 16>()); break;
+    case 32: go(std::integral_constant<int, 32>()); break;
+    case 64: go(std::integral_constant<int, 64>()); break;
+    case 128: go(std::integral_constant<int, 128>()); break;
+    case 256: go(std::integral_constant<int, 256>()); break;
+    case 512: go(std::integral_constant<int, 512>()); break;
+    default: go(std::integral_constant<int, 1024>()); break;
+  }
+}
+
+}  // namespace
+
+bool norm_dim_ok(int D) { return D >= 1 && D <= kMaxD; }
+
+int64_t norm_bwd_parts(int64_t rows, int D) {
+  const int tpr = tpr_of(D);
+  return grid_of(rows, tpr, per_sm_of(tpr));
+}
+
+cudaError_t launch_gated_norm_fwd(const void* x, int x_f32, const void* z, const void* w, int w_bf16, void* y,
+                                  int64_t rows, int D, float eps, cudaStream_t stream) {
+  const int tpr = tpr_of(D);
+  const unsigned grid = (unsigned)grid_of(rows, tpr, 2048 / threads_of(tpr));
+  const bool vec = vec_ok(D, {x, z, w, y});
+  dispatch(tpr, vec, [&](auto T, auto V) {
+    constexpr int TPR = decltype(T)::value;
+    constexpr bool VEC = decltype(V)::value;
+    const auto zb = static_cast<const __nv_bfloat16*>(z);
+    const auto yb = static_cast<__nv_bfloat16*>(y);
+    if (x_f32)
+      gated_norm_fwd_kernel<TPR, VEC, float><<<grid, threads_of(TPR), 0, stream>>>(
+          static_cast<const float*>(x), zb, w, w_bf16, yb, rows, D, eps);
+    else
+      gated_norm_fwd_kernel<TPR, VEC, __nv_bfloat16><<<grid, threads_of(TPR), 0, stream>>>(
+          static_cast<const __nv_bfloat16*>(x), zb, w, w_bf16, yb, rows, D, eps);
+  });
+  return cudaGetLastError();
+}
+
+cudaError_t launch_gated_norm_bwd(const void* dy, const void* x, int x_f32, const void* z, const void* w, int w_bf16,
+                                  void* dx, void* dz, float* dw, int64_t rows, int D, float eps, float* part,
+                                  cudaStream_t stream) {
+  const int tpr = tpr_of(D);
+  const unsigned grid = (unsigned)norm_bwd_parts(rows, D);
+  const bool vec = vec_ok(D, {dy, x, z, w, dx, dz});
+  dispatch(tpr, vec, [&](auto T, auto V) {
+    constexpr int TPR = decltype(T)::value;
+    constexpr bool VEC = decltype(V)::value;
+    const auto dyb = static_cast<const __nv_bfloat16*>(dy), zb = static_cast<const __nv_bfloat16*>(z);
+    const auto dzb = static_cast<__nv_bfloat16*>(dz);
+    if (x_f32)
+      gated_norm_bwd_kernel<TPR, VEC, float><<<grid, threads_of(TPR), 0, stream>>>(
+          dyb, static_cast<const float*>(x), zb, w, w_bf16, static_cast<float*>(dx), dzb, part, rows, D, eps);
+    else
+      gated_norm_bwd_kernel<TPR, VEC, __nv_bfloat16><<<grid, threads_of(TPR), 0, stream>>>(
+          dyb, static_cast<const __nv_bfloat16*>(x), zb, w, w_bf16, static_cast<__nv_bfloat16*>(dx), dzb, part, rows, D,
+          eps);
+  });
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  sum_partials_kernel<<<dim3((D + 7) / 8, 1), 256, 0, stream>>>(part, nullptr, dw, nullptr, (int)grid, D);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_residual_norm_fwd(const void* y, const void* h, int h_f32, const void* w_post, const void* w_pre,
+                                     int w_bf16, void* h_out, void* x, int64_t rows, int D, float alpha, float eps,
+                                     cudaStream_t stream) {
+  const int tpr = tpr_of(D);
+  const unsigned grid = (unsigned)grid_of(rows, tpr, 2048 / threads_of(tpr));
+  const bool vec = vec_ok(D, {y, h, w_post, w_pre, h_out, x});
+  dispatch(tpr, vec, [&](auto T, auto V) {
+    constexpr int TPR = decltype(T)::value;
+    constexpr bool VEC = decltype(V)::value;
+    const auto yb = static_cast<const __nv_bfloat16*>(y);
+    const auto xb = static_cast<__nv_bfloat16*>(x);
+    auto go = [&](auto P, auto* tag) {
+      using H = std::remove_pointer_t<decltype(tag)>;
+      residual_norm_fwd_kernel<TPR, VEC, decltype(P)::value, H><<<grid, threads_of(TPR), 0, stream>>>(
+          yb, static_cast<const H*>(h), w_post, w_pre, w_bf16, static_cast<H*>(h_out), xb, rows, D, alpha, eps);
+    };
+    if (h_f32) w_post ? go(std::true_type(), (float*)nullptr) : go(std::false_type(), (float*)nullptr);
+    else w_post ? go(std::true_type(), (__nv_bfloat16*)nullptr) : go(std::false_type(), (__nv_bfloat16*)nullptr);
+  });
+  return cudaGetLastError();
+}
+
+cudaError_t launch_residual_norm_bwd(const void* dx, const void* dh_out, const void* y, const void* h, int h_f32,
+                                     const void* w_post, const void* w_pre, int w_bf16, void* dy, void* dh,
+                                     float* dw_post, float* dw_pre, int64_t rows, int D, float alpha, float eps,
+                                     float* part, cudaStream_t stream) {
+  const int tpr = tpr_of(D);
+  const unsigned grid = (unsigned)norm_bwd_parts(rows, D);
+  const bool vec = vec_ok(D, {dx, dh_out, y, h, w_post, w_pre, dy, dh});
+  float* const part2 = part + (int64_t)grid * D;
+  dispatch(tpr, vec, [&](auto T, auto V) {
+    constexpr int TPR = decltype(T)::value;
+    constexpr bool VEC = decltype(V)::value;
+    const auto dxb = static_cast<const __nv_bfloat16*>(dx), yb = static_cast<const __nv_bfloat16*>(y);
+    const auto dyb = static_cast<__nv_bfloat16*>(dy);
+    auto go = [&](auto P, auto* tag) {
+      using H = std::remove_pointer_t<decltype(tag)>;
+      residual_norm_bwd_kernel<TPR, VEC, decltype(P)::value, H><<<grid, threads_of(TPR), 0, stream>>>(
+          dxb, static_cast<const H*>(dh_out), yb, static_cast<const H*>(h), w_post, w_pre, w_bf16, dyb,
+          static_cast<H*>(dh), part, part2, rows, D, alpha, eps);
+    };
+    if (h_f32) w_post ? go(std::true_type(), (float*)nullptr) : go(std::false_type(), (float*)nullptr);
+    else w_post ? go(std::true_type(), (__nv_bfloat16*)nullptr) : go(std::false_type(), (__nv_bfloat16*)nullptr);
+  });
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  sum_partials_kernel<<<dim3((D + 7) / 8, w_post ? 2 : 1), 256, 0, stream>>>(part, part2, dw_pre, dw_post, (int)grid,
+                                                                            D);
+  return cudaGetLastError();
+}
+
+}  // namespace gdn

@@ -34,7 +34,10 @@ EXPORTED = ("gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_noal
             "gdn_prefill_decode_workspace_size", "gdn_prefill_decode_fwd",
             "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_chunk_bwd",
             "kda_prefill_decode_workspace_size", "kda_prefill_decode_fwd",
-            "gdn_decode_step", "fp8_tile_qdq", "int8_block_qdq", "gdn_status_string", "gdn_check_device_status")
+            "gdn_decode_step", "fp8_tile_qdq", "int8_block_qdq", "gdn_status_string", "gdn_check_device_status",
+            "la_chunk_fwd_workspace_size", "la_chunk_bwd_workspace_size", "la_chunk_fwd", "la_chunk_bwd",
+            "la_decode_step", "gated_norm_fwd", "gated_norm_bwd_workspace_size", "gated_norm_bwd",
+            "residual_norm_fwd", "residual_norm_bwd_workspace_size", "residual_norm_bwd")
 
 
 class GdnError(RuntimeError):
@@ -56,6 +59,20 @@ class ChunkArgs(ctypes.Structure):
 class ChunkGrads(ctypes.Structure):
     _fields_ = [("dout", ctypes.c_void_p), ("dhT", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
                 ("dv", ctypes.c_void_p), ("dg", ctypes.c_void_p), ("dbeta", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
+
+
+class LaArgs(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("g", ctypes.c_void_p),
+                ("h0", ctypes.c_void_p), ("cu_seqlens", ctypes.c_void_p), ("cu_seqlens_host", ctypes.c_void_p),
+                ("o", ctypes.c_void_p), ("hT", ctypes.c_void_p),
+                ("B", ctypes.c_int32), ("T", ctypes.c_int32), ("N", ctypes.c_int32), ("Hqk", ctypes.c_int32),
+                ("Hv", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class LaGrads(ctypes.Structure):
+    _fields_ = [("dout", ctypes.c_void_p), ("dhT", ctypes.c_void_p), ("dq", ctypes.c_void_p), ("dk", ctypes.c_void_p),
+                ("dv", ctypes.c_void_p), ("dg", ctypes.c_void_p), ("dh0", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -102,6 +119,21 @@ def load(build_if_missing: bool = True):
         lib.fp8_tile_qdq.argtypes = [P, P, P, ctypes.c_int64, I32, I32, I32, P]
         lib.int8_block_qdq.restype = ctypes.c_int
         lib.int8_block_qdq.argtypes = [P, P, P, ctypes.c_int64, I32, I32, P]
+        I64, SZ = ctypes.c_int64, ctypes.c_size_t
+        LA, LG = ctypes.POINTER(LaArgs), ctypes.POINTER(LaGrads)
+        for fn, res, args in (
+                ("la_chunk_fwd_workspace_size", SZ, [LA]), ("la_chunk_bwd_workspace_size", SZ, [LA]),
+                ("la_chunk_fwd", ctypes.c_int, [LA, P, SZ, P]), ("la_chunk_bwd", ctypes.c_int, [LA, LG, P, SZ, P]),
+                ("la_decode_step", ctypes.c_int, [P] * 7 + [I32] * 5 + [F, U32, P]),
+                ("gated_norm_fwd", ctypes.c_int, [P, I32, P, P, I32, P, I64, I32, F, P]),
+                ("gated_norm_bwd_workspace_size", SZ, [I64, I32]),
+                ("gated_norm_bwd", ctypes.c_int, [P, P, I32, P, P, I32, P, P, P, I64, I32, F, P, SZ, P]),
+                ("residual_norm_fwd", ctypes.c_int, [P, P, I32, P, P, I32, P, P, I64, I32, F, F, P]),
+                ("residual_norm_bwd_workspace_size", SZ, [I64, I32]),
+                ("residual_norm_bwd", ctypes.c_int,
+                 [P, P, P, P, I32, P, P, I32, P, P, P, P, I64, I32, F, F, P, SZ, P])):
+            getattr(lib, fn).restype = res
+            getattr(lib, fn).argtypes = args
         lib.gdn_status_string.restype = ctypes.c_char_p
         lib.gdn_status_string.argtypes = [ctypes.c_int]
         lib.gdn_check_device_status.restype = ctypes.c_int

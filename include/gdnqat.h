@@ -252,6 +252,90 @@ gdn_status fp8_tile_qdq(const float* x, float* y, float* scales, int64_t lead, i
 gdn_status int8_block_qdq(const float* x, float* y, float* scales, int64_t rows, int32_t cols,
                           int32_t block_cols, gdn_stream_t stream);
 
+/* ---- Linear attention with a decay for each head ----
+ * Per sequence n and value head h, state S in R^{dk x dv}, a_t = exp(g_t):
+ *     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = scale * S_t^T q_t
+ * (the gated delta rule above without its correction by S^T k). Conventions as above, with o and
+ * the gradients of q, k, v in bf16, the type of the tensors that they stand beside; states and
+ * the gradient of g are fp32. g <= 0; g = -inf (a = 0) starts the state anew at that token. A
+ * value of g below -110 is taken as -110 (exp is zero there in fp32). */
+
+/* g is fp32 [Hv], one fixed decay per head for all tokens and sequences, and so is its gradient. */
+#define LA_FLAG_HEAD_DECAY 1u
+
+typedef struct {
+  const void* q;               /* device bf16 [B, T, Hqk, dk] */
+  const void* k;               /* device bf16 [B, T, Hqk, dk] */
+  const void* v;               /* device bf16 [B, T, Hv, dv] */
+  const float* g;              /* device fp32 log-decay [B, T, Hv] (LA_FLAG_HEAD_DECAY: [Hv]) */
+  const float* h0;             /* device fp32 [N, Hv, dk, dv]; NULL = zero initial state */
+  const int32_t* cu_seqlens;   /* device int32 [N + 1]; NULL = dense batch (N == B) */
+  const int32_t* cu_seqlens_host; /* host copy of cu_seqlens (required with it): validated before launch */
+  void* o;                     /* device bf16 [B, T, Hv, dv] (forward); must not alias any input */
+  float* hT;                   /* device fp32 [N, Hv, dk, dv] or NULL (forward); may alias h0 exactly */
+  int32_t B, T, N, Hqk, Hv, dk, dv;   /* dk, dv in {64, 128}; Hv a multiple of Hqk */
+  float scale;
+  uint32_t flags;              /* LA_FLAG_HEAD_DECAY */
+} la_chunk_args;
+
+typedef struct {
+  const void* dout;            /* device bf16 [B, T, Hv, dv]: gradient of o */
+  const float* dhT;            /* device fp32 [N, Hv, dk, dv]: gradient of hT, or NULL (zero) */
+  void* dq;                    /* device bf16 [B, T, Hqk, dk]: summed over the value heads of a q/k head */
+  void* dk;                    /* device bf16 [B, T, Hqk, dk]: likewise */
+  void* dv;                    /* device bf16 [B, T, Hv, dv] */
+  float* dg;                   /* device fp32, the shape of g */
+  float* dh0;                  /* device fp32 [N, Hv, dk, dv] or NULL */
+} la_chunk_grads;
+
+/* Device workspace of la_chunk_fwd / la_chunk_bwd in bytes; 0 for invalid arguments. Depends on
+ * sizes and flags only. Contents need no initialization. */
+size_t la_chunk_fwd_workspace_size(const la_chunk_args* args);
+size_t la_chunk_bwd_workspace_size(const la_chunk_args* args);
+/* o for every token and (hT) the final state of every sequence; empty sequences give hT = h0.
+ * workspace: device, 256-byte aligned. gdn_check_device_status reads its status word. */
+gdn_status la_chunk_fwd(const la_chunk_args* args, void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+/* The gradients of <o, dout> + <hT, dhT>; args: the forward's inputs (o and hT are not read). */
+gdn_status la_chunk_bwd(const la_chunk_args* args, const la_chunk_grads* grads, void* workspace,
+                        size_t workspace_bytes, gdn_stream_t stream);
+/* One token per sequence. q, k: device bf16 [N, Hqk, dk]; v: device bf16 [N, Hv, dv]; g: device fp32
+ * [N, Hv]; state, state_out: device fp32 [N, Hv, dk, dv], the same or disjoint; o: device bf16
+ * [N, Hv, dv]. o is taken from the updated state, which is then QDQ'd (GDN_FLAG_STATE_QDQ: E4M3 tiles;
+ * with GDN_FLAG_STATE_INT8: INT8 blocks; scale = fl(amax fl(1 / 448)) or fl(amax fl(1 / 127)), 1 if
+ * that is zero, code = that of fl(x / scale), all in fp32) and stored. dk in {64, 128}, dv in {64, 128, 256}. */
+gdn_status la_decode_step(const void* q, const void* k, const void* v, const float* g, const float* state,
+                          float* state_out, void* o, int32_t N, int32_t Hqk, int32_t Hv, int32_t dk, int32_t dv,
+                          float scale, uint32_t flags, gdn_stream_t stream);
+
+/* ---- RMS norms around a block ----
+ * Rows of D elements (1 <= D <= 8192), contiguous, any alignment to the element; rms(x) = x /
+ * sqrt(mean(x^2) + eps) per row, in fp32; each output is rounded once. Tensors marked x/h have the
+ * type of the _dtype argument, w's that of w_dtype, y, z and their gradients are bf16; gradients
+ * of weights are fp32. Outputs must not overlap inputs, except that h_out may be h and dh may be dh_out. */
+typedef enum { GDN_DTYPE_BF16 = 0, GDN_DTYPE_F32 = 1 } gdn_dtype;
+
+/* y = rms(x) w silu(z): the norm behind a mixing core and its gate; a row is a (token, head). */
+gdn_status gated_norm_fwd(const void* x, int32_t x_dtype, const void* z, const void* w, int32_t w_dtype, void* y,
+                          int64_t rows, int32_t D, float eps, gdn_stream_t stream);
+size_t gated_norm_bwd_workspace_size(int64_t rows, int32_t D);   /* 0 for invalid sizes */
+/* dx (type of x), dz, dw [D] from dy. workspace: device, 16-byte aligned. */
+gdn_status gated_norm_bwd(const void* dy, const void* x, int32_t x_dtype, const void* z, const void* w,
+                          int32_t w_dtype, void* dx, void* dz, float* dw, int64_t rows, int32_t D, float eps,
+                          void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
+/* h_out = h + alpha n, n = rms(y) w_post (w_post NULL: n = y); x = rms(h_out) w_pre, from the h_out
+ * before its rounding: the norm after a block, its scaled residual and the norm before the next. */
+gdn_status residual_norm_fwd(const void* y, const void* h, int32_t h_dtype, const void* w_post, const void* w_pre,
+                             int32_t w_dtype, void* h_out, void* x, int64_t rows, int32_t D, float alpha, float eps,
+                             gdn_stream_t stream);
+size_t residual_norm_bwd_workspace_size(int64_t rows, int32_t D);   /* 0 for invalid sizes */
+/* dy, dh (type of h), dw_post [D] (NULL without w_post), dw_pre [D] from dx and dh_out (type of h; NULL
+ * = zero). y and h are the forward's inputs; h_out is recomputed from them. */
+gdn_status residual_norm_bwd(const void* dx, const void* dh_out, const void* y, const void* h, int32_t h_dtype,
+                             const void* w_post, const void* w_pre, int32_t w_dtype, void* dy, void* dh,
+                             float* dw_post, float* dw_pre, int64_t rows, int32_t D, float alpha, float eps,
+                             void* workspace, size_t workspace_bytes, gdn_stream_t stream);
+
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status status);
 
