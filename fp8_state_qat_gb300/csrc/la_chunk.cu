@@ -1,0 +1,239 @@
+// la_chunk.cu -- chunked linear attention with a decay for each head: the launches of the forward and of
+// its gradients, and the gradient of the decays.
+//
+// Forward: the states entering the chunks (la_state.cu), then o (la_out.cu, role o).
+// Backward: the states entering the chunks, the state gradients leaving them, then dq, dk, dv
+// (la_out.cu, three roles), then dg, and with shared q/k heads the sums over their value heads.
+//
+// dg. o depends on g_t through every decay that spans token t: with (i < t <= j) all pairs of a chunk,
+//   dg_t = sum_{i < t <= j} m_ji + sum_{j >= t} a_j + sum_{i < t} b_i + exp(gam_C) <S, dS>,
+//   m_ji = scale D (q_j . k_i)(do_j . v_i),  a_j = q_j . (state part of dq_j),  b_i = k_i . (state part of dk_i),
+// S entering and dS leaving the chunk. With r_j, c_i the row and column sums of m (i != j) the first
+// sum is sum_{j >= t} (r_j - c_j). No term is larger than the decayed products themselves, where the
+// usual suffix sum of q . dq - k . dk over the whole sequence subtracts undecayed ones.
+#include <algorithm>
+
+#include "kernels.h"
+#include "la_chunk.cuh"
+
+namespace gdn {
+namespace la {
+namespace {
+
+struct DgParams {
+  Seqs seqs;
+  GateSrc gates;
+  const float *rq, *rk, *aq, *bk;        // per (token, head): r, c, a, b
+  const __nv_bfloat16 *S, *dS;           // two terms each
+  float* dg;                             // [tokens, Hv], or per item with head_decay
+  int64_t elems;                         // dk dv
+};
+
+// One CTA of 128 threads per (chunk slot, head): thread = token.
+__global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
+  const int64_t item = blockIdx.x;
+  const int Hv = p.gates.Hv, h = (int)(item % Hv);
+  const int64_t slot = item / Hv;
+  int lo = 0, hi = p.seqs.N - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.seqs.slot0(mid) <= slot) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t c = slot - p.seqs.slot0(lo), len = p.seqs.len(lo), tok = p.seqs.start(lo) + c * kC;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  if (c < 0 || c * kC >= len) {
+    if (p.gates.head_decay && t == 0) p.dg[item] = 0.f;
+    return;
+  }
+  const int L = (int)(len - c * kC < kC ? len - c * kC : kC);
+  __shared__ float red[3][4];
+  float gx[4];
+  Gates g;
+  p.gates.load(gx, tok, h, L, lane);
+  scan_gates(gx, g, lane);
+  const float decay = expf((g.tot(0) + g.tot(1)) + (g.tot(2) + g.tot(3)));
+  // <S, dS>, where the decay across the chunk leaves anything of it
+  float x = 0.f;
+  if (decay > 0.f) {
+    const uint4* s = reinterpret_cast<const uint4*>(p.S + item * 2 * p.elems);
+    const uint4* d = reinterpret_cast<const uint4*>(p.dS + item * 2 * p.elems);
+    const int n8 = (int)(p.elems / 8);
+#pragma unroll 2
+    for (int i = t; i < n8; i += kC) {
+      const uint4 q[4] = {s[i], s[i + n8], d[i], d[i + n8]};
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 a = unpack_bf16(w[e]), al = unpack_bf16(w[4 + e]), b = unpack_bf16(w[8 + e]), bl = unpack_bf16(w[12 + e]);
+        x = fmaf(a.x + al.x, b.x + bl.x, x);
+        x = fmaf(a.y + al.y, b.y + bl.y, x);
+      }
+    }
+  }
+  const int64_t at = (tok + t) * Hv + h;
+  float f = 0.f, b = 0.f;
+  if (t < L) {
+    f = (p.rq[at] - p.rk[at]) + p.aq[at];
+    b = p.bk[at];
+  }
+  float fs = f, bs = b;   // suffix sums of f, prefix sums of b, both with the own token
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const float yf = __shfl_down_sync(0xffffffffu, fs, off), yb = __shfl_up_sync(0xffffffffu, bs, off);
+    if (lane + off < 32) fs += yf;
+    if (lane >= off) bs += yb;
+  }
+  x = warp_sum(x);
+  if (lane == 0) {
+    red[0][warp] = fs;
+    red[2][warp] = x;
+  }
+  if (lane == 31) red[1][warp] = bs;
+  __syncthreads();
+  float v = fs + (bs - b);
+  float before = 0.f, after = 0.f;
+  for (int w = 0; w < 4; ++w) {
+    if (w > warp) after += red[0][w];
+    if (w < warp) before += red[1][w];
+  }
+  v = (v + (after + before)) + decay * ((red[2][0] + red[2][1]) + (red[2][2] + red[2][3]));
+  if (!p.gates.head_decay) {
+    if (t < L) p.dg[at] = v;
+    return;
+  }
+  v = warp_sum(t < L ? v : 0.f);
+  __syncthreads();
+  if (lane == 0) red[0][warp] = v;
+  __syncthreads();
+  if (t == 0) p.dg[item] = (red[0][0] + red[0][1]) + (red[0][2] + red[0][3]);
+}
+
+// dg of a fixed decay: the sum over all chunks, 256 threads in a fixed order, in 64 bits
+__global__ void __launch_bounds__(256) la_dg_head_kernel(const float* part, float* dg, int64_t slots, int Hv) {
+  __shared__ double red[256];
+  const int h = blockIdx.x, t = threadIdx.x;
+  double s = 0.;
+  for (int64_t i = t; i < slots; i += 256) s += part[i * Hv + h];
+  red[t] = s;
+  __syncthreads();
+  for (int n = 128; n > 0; n >>= 1) {
+    if (t < n) red[t] += red[t + n];
+    __syncthreads();
+  }
+  if (t == 0) dg[h] = (float)red[0];
+}
+
+// dq and dk (blockIdx.y) of a shared head: the sum over its value heads, four channels a thread
+__global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, const float* x1, __nv_bfloat16* y0,
+                                                           __nv_bfloat16* y1, int64_t quads, int G, int D4) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= quads) return;
+  const float4* x = reinterpret_cast<const float4*>(blockIdx.y ? x1 : x0);
+  const int64_t row = i / D4, d = i % D4;
+  float4 s = x[row * G * D4 + d];
+  for (int j = 1; j < G; ++j) {
+    const float4 v = x[(row * G + j) * D4 + d];
+    s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+  }
+  reinterpret_cast<uint2*>(blockIdx.y ? y1 : y0)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
+}
+
+size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
+
+struct Layout {
+  size_t S, dS, tot, dec, rq, rk, aq, bk, pq, pk, item, total;
+};
+Layout layout_of(const LaProblem& p, bool bwd) {
+  const size_t items = (size_t)la_slots(p) * p.Hv, elems = (size_t)p.dk * p.dv, th = (size_t)p.B * p.T * p.Hv;
+  const int nseg = state_segments(p);
+  Layout l{};
+  size_t at = kStatusBytes;
+  auto take = [&](size_t n) {
+    const size_t here = at;
+    at += up(n);
+    return here;
+  };
+  l.S = take(items * elems * 2 * (bwd ? 2 : 1));
+  if (bwd) l.dS = take(items * elems * 4);
+  if (nseg > 1) {
+    l.tot = take((size_t)p.N * p.Hv * nseg * elems * 4);
+    l.dec = take((size_t)p.N * p.Hv * nseg * 4);
+  }
+  if (bwd) {
+    l.rq = take(th * 4);
+    l.rk = take(th * 4);
+    l.aq = take(th * 4);
+    l.bk = take(th * 4);
+    if (p.Hv != p.Hqk) {
+      l.pq = take(th * p.dk * 4);
+      l.pk = take(th * p.dk * 4);
+    }
+    if (p.head_decay) l.item = take(items * 4);
+  }
+  l.total = at;
+  return l;
+}
+
+}  // namespace
+}  // namespace la
+
+using namespace la;
+
+size_t la_fwd_workspace(const LaProblem& p) { return layout_of(p, false).total; }
+size_t la_bwd_workspace(const LaProblem& p) { return layout_of(p, true).total; }
+
+cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
+  unsigned char* const base = static_cast<unsigned char*>(ws);
+  const Layout l = layout_of(p, false);
+  int* const status = static_cast<int*>(ws);
+  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec)};
+  // o reads h0 through the states alone, so hT may be h0
+  if ((e = launch_states(p, s, status, stream)) != cudaSuccess) return e;
+  OutRun o{p.q, p.k, p.v, nullptr, {base + l.S, nullptr}, {1, 1}, {}, 1};
+  o.role[0] = {0, 1, 2, -1, 0, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
+  return launch_outputs(p, o, status, stream);
+}
+
+cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaStream_t stream) {
+  unsigned char* const base = static_cast<unsigned char*>(ws);
+  const Layout l = layout_of(p, true);
+  int* const status = static_cast<int*>(ws);
+  const int64_t tokens = (int64_t)p.B * p.T, items = la_slots(p) * p.Hv;
+  const int G = p.Hv / p.Hqk;
+  float *tot = (float*)(base + l.tot), *dec = (float*)(base + l.dec);
+  float *rq = (float*)(base + l.rq), *rk = (float*)(base + l.rk), *aq = (float*)(base + l.aq), *bk = (float*)(base + l.bk);
+  float *pq = (float*)(base + l.pq), *pk = (float*)(base + l.pk);
+  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
+  if (e != cudaSuccess) return e;
+  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec};
+  if ((e = launch_states(p, f, status, stream)) != cudaSuccess) return e;
+  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec};
+  if ((e = launch_states(p, b, status, stream)) != cudaSuccess) return e;
+  if (tokens == 0 || items == 0)
+    return p.head_decay ? cudaMemsetAsync(gr.dg, 0, (size_t)p.Hv * 4, stream) : cudaSuccess;
+  OutRun o{p.q, p.k, p.v, gr.dout, {base + l.S, base + l.dS}, {2, 2}, {}, 3};
+  o.role[0] = {3, 2, 1, 0, 0, 1, 0, p.scale, p.scale, G > 1 ? (void*)pq : gr.dq, G > 1, rq, aq};
+  o.role[1] = {2, 3, 0, 1, 1, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
+  o.role[2] = {1, 0, 3, -1, 1, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
+  if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
+  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, (const __nv_bfloat16*)(base + l.S),
+             (const __nv_bfloat16*)(base + l.dS), p.head_decay ? (float*)(base + l.item) : gr.dg, (int64_t)p.dk * p.dv};
+  la_dg_kernel<<<(unsigned)items, kC, 0, stream>>>(d);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.head_decay) {
+    la_dg_head_kernel<<<(unsigned)p.Hv, 256, 0, stream>>>((const float*)(base + l.item), gr.dg, la_slots(p), p.Hv);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (G > 1) {
+    const int64_t quads = tokens * p.Hqk * (p.dk / 4);
+    la_group_sum_kernel<<<dim3((unsigned)((quads + 255) / 256), 2), 256, 0, stream>>>(
+        pq, pk, (__nv_bfloat16*)gr.dq, (__nv_bfloat16*)gr.dk, quads, G, p.dk / 4);
+    e = cudaGetLastError();
+  }
+  return e;
+}
+
+}  // namespace gdn

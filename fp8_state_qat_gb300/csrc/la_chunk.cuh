@@ -1,0 +1,147 @@
+// la_chunk.cuh -- pieces shared by the chunked linear-attention kernels (128-token chunks).
+#pragma once
+
+#include "common.cuh"
+#include "la.h"
+#include "tc_common.cuh"
+#include "tc_epilogue.cuh"
+
+namespace gdn {
+namespace la {
+
+constexpr int kC = 128;                      // tokens a chunk: the M of one full tcgen05 product
+constexpr uint32_t kBlk = 16 * 1024;         // a [128 tokens][64 channels] bf16 block, 128-byte rows
+constexpr uint32_t kTile = 2 * kBlk;
+
+// The chunk slots of sequence n start at start(n) / 128 + n: unique, and known without a table.
+struct Seqs {
+  const int32_t* cu;   // device cu_seqlens, or null: N sequences of T tokens
+  int T, N;
+  __device__ __forceinline__ int64_t start(int n) const { return cu ? (int64_t)cu[n] : (int64_t)n * T; }
+  __device__ __forceinline__ int64_t len(int n) const { return cu ? (int64_t)cu[n + 1] - cu[n] : (int64_t)T; }
+  __device__ __forceinline__ int64_t slot0(int n) const { return start(n) / kC + n; }
+};
+
+// exp(g) below -110 is zero in fp32; the bound keeps prefix sums finite where g = -inf resets a state
+// (a NaN stays one)
+__device__ __forceinline__ float gate(float g) { return g < -110.f ? -110.f : g; }
+
+// Prefix sums of a chunk's log-decays within its four 32-token blocks, by one warp: lane l holds
+// token 32 j + l. Each is a pair hi + lo, so that a difference of two of them keeps its accuracy when a
+// large |g| (a reset) lies before both; decays across blocks are products of exponentials of
+// sums <= 0 of such differences, so nothing overflows and nothing cancels.
+struct Gates {
+  float hi[4], lo[4];   // inclusive prefix of the block
+  float thi[4], tlo[4]; // the block's total
+  __device__ __forceinline__ float tot(int j) const { return thi[j] + tlo[j]; }
+  // sum over the tokens after this lane's token of block j, up to the block's end
+  __device__ __forceinline__ float after(int j) const { return (thi[j] - hi[j]) + (tlo[j] - lo[j]); }
+  __device__ __forceinline__ float pre(int j) const { return hi[j] + lo[j]; }
+};
+
+struct GateSrc {
+  const float* g;
+  int Hv, head_decay;
+  __device__ __forceinline__ void load(float (&x)[4], int64_t tok, int h, int L, int lane) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 32 * j + lane;
+      x[j] = t < L ? gate(head_decay ? g[h] : g[(tok + t) * Hv + h]) : 0.f;
+    }
+  }
+};
+
+__device__ __forceinline__ void scan_gates(const float (&x)[4], Gates& w, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float s = x[j], e = 0.f;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const float ys = __shfl_up_sync(0xffffffffu, s, off), ye = __shfl_up_sync(0xffffffffu, e, off);
+      if (lane >= off) {
+        const float t = __fadd_rn(s, ys), b = __fsub_rn(t, s);     // two-sum: t + err = s + ys exactly
+        e += ye + __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(ys, b));
+        s = t;
+      }
+    }
+    w.hi[j] = s;
+    w.lo[j] = e;
+    w.thi[j] = __shfl_sync(0xffffffffu, s, 31);
+    w.tlo[j] = __shfl_sync(0xffffffffu, e, 31);
+  }
+}
+
+// tcgen05 product with A in tensor memory (lane = row of A, each 32-bit column two bf16 of K)
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(
+          d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// rows [L, 128) of a tile of `blocks` [128][64] blocks become zero (thread t of 128: row t)
+__device__ __forceinline__ void zero_tail_rows(unsigned char* tile, int blocks, int t, int L) {
+  if (t >= L && t < kC) {
+    for (int b = 0; b < blocks; ++b)
+#pragma unroll
+      for (int c = 0; c < 8; ++c)
+        *reinterpret_cast<uint4*>(tile + b * kBlk + (t >> 3) * 1024 + (t & 7) * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+  }
+}
+
+// ---- launchers of the parts (la_state.cu, la_out.cu) ----
+// States at chunk boundaries, bf16 terms per item = slot * Hv + h: [term][dv / 64][dk][64].
+struct StateRun {
+  const void* x;        // bf16 [tokens, Hqk, dk]: k forwards, q backwards
+  const void* y;        // bf16 [tokens, Hv, dv]: v forwards, dout backwards
+  const float* s0;      // [N, Hv, dk, dv] or null
+  float* sT;            // [N, Hv, dk, dv] or null
+  void* states;         // the state before each chunk's own contribution, or null
+  int terms;            // bf16 terms stored: 1 (rounded) or 2 (hi + lo)
+  int reverse;
+  float scale;          // weight of every token's contribution
+  float* seg_tot;       // split walks: [N Hv][nseg][dk][dv]
+  float* seg_dec;       // [N Hv][nseg]
+};
+int state_segments(const LaProblem& p);
+cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream);
+
+// One family of outputs: out_t = f_in sum_s decay(t, s) (a_t . b_s) c_s + f_st decay_t a_t^T St,
+// s <= t with the state before the chunk (reverse 0), or s >= t with the state after it (reverse 1).
+struct Role {
+  int a, b, c, e;        // which of the maps q, k, v, do (0-3); e: rows dotted with the outputs, or -1
+  int st;                // which states (0: S, 1: dS)
+  int st_transposed;     // St = S^T: the product is over the value columns
+  int reverse;
+  float f_in, f_st;
+  void* out;             // bf16 [tokens, Hv, dc] (fp32 with out_f32)
+  int out_f32;
+  float* dot_in;         // with e: sum_{s != t} decay (a_t . b_s) (e_t . c_s) f_in per (token, head)
+  float* dot_st;         // with e: e_t . (the state part of out_t)
+};
+struct OutRun {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* dout;
+  const void* states[2];
+  int terms[2];
+  Role role[3];
+  int roles;
+};
+cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cudaStream_t stream);
+
+int64_t la_slots(const LaProblem& p);
+
+}  // namespace la
+}  // namespace gdn

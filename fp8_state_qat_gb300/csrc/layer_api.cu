@@ -47,9 +47,9 @@ gdn_status validate_la_sizes(const la_chunk_args* a) {
   if (a->Hv % a->Hqk || (a->flags & ~LA_FLAG_HEAD_DECAY)) return GDN_ERR_INVALID_ARG;
   if ((a->dk != 64 && a->dk != 128) || (a->dv != 64 && a->dv != 128)) return GDN_ERR_UNSUPPORTED_SHAPE;
   const int64_t tokens = (int64_t)a->B * a->T;
-  // token indexes, chunk slots times heads and sequence-head pairs are kept in 32 bits
-  if (tokens > 0x7fffffff - 256 || (tokens / 64 + a->N) * (int64_t)a->Hv > 0x7fffffff / 4 || a->Hv > 65535)
-    return GDN_ERR_INVALID_ARG;
+  // TMA coordinates are 32-bit: tokens, and the rows of the stored states (512 a chunk and head at most,
+  // 64 KB: more would not fit the device either)
+  if (tokens > 0x7fffffff - 256 || (tokens / 128 + a->N) * (int64_t)a->Hv > 0x3fffff) return GDN_ERR_INVALID_ARG;
   if (a->cu_seqlens) {
     if (a->B != 1 || a->N < 1 || !a->cu_seqlens_host) return GDN_ERR_INVALID_ARG;
     const int32_t* c = a->cu_seqlens_host;

@@ -84,7 +84,7 @@ def test_heads_and_widths(gdn, dk, dv, Hqk, Hv):
 
 
 @pytest.mark.parametrize("head", [False, True])
-@pytest.mark.parametrize("lens", [[1], [5, 0, 1, 130, 64, 0], [0, 0], [257, 3, 128, 127, 129, 1, 1, 40]])
+@pytest.mark.parametrize("lens", [[1], [5, 0, 1, 130, 64, 0], [0, 0], [257, 3, 128, 127, 129, 1, 1, 40], [0, 700]])
 def test_packed_sequences(gdn, lens, head):
     check_all(gdn, *inputs(1, 0, 2, 4, 64, 128, seed=sum(lens), lens=lens, head=head), 1.0)
 
@@ -105,6 +105,11 @@ def test_many_chunks_few_heads(gdn):
     check_all(gdn, *inputs(1, 0, 1, 2, 128, 128, seed=10, lens=[3100, 17, 0, 1500]), 1.0)
 
 
+def test_slow_decay(gdn):
+    """Memories of thousands of tokens: the state carries over many chunks."""
+    check_all(gdn, *inputs(1, 2500, 1, 2, 128, 64, seed=11, g_mean=8.0), 1.0)
+
+
 def test_no_decay(gdn):
     x, gr = inputs(1, 700, 1, 2, 64, 64, seed=12)
     x["g"] = torch.zeros_like(x["g"])
@@ -117,6 +122,20 @@ def _check_strong(gdn, x, gr):
     check(got, want, ["o", "hT", "dq", "dk", "dv", "dh0"])
     size = max(want["dg"].norm().item(), 1e-3 * (want["dq"] * x["q"].double()).norm().item())
     assert (got["dg"].cpu().double() - want["dg"]).norm().item() <= TOL["dg"] * size
+
+
+@pytest.mark.parametrize("value", [-20.0, -60.0, -200.0, -3.0e38, -float("inf")])
+def test_strong_decay_everywhere(gdn, value):
+    x, gr = inputs(1, 260, 2, 2, 64, 64, seed=13)
+    x["g"] = torch.full_like(x["g"], value)
+    x["h0"][:, :, 0, 0] = 1.0   # dh0 and hT stay nonzero below
+    got = {**dict(zip(("o", "hT"), run_fwd(gdn, x, 1.0))), **run_bwd(gdn, x, gr, 1.0)}
+    want = ref.la(*(x[n] for n in ("q", "k", "v", "g", "h0", "cu")), 1.0, gr["dout"], gr["dhT"])
+    check(got, want, ["o", "hT", "dq", "dk", "dv"])
+    # dh0 and dg are e^value times the size of the other gradients, zero where that is zero in fp32
+    assert (got["dh0"].cpu().double() - want["dh0"]).norm().item() <= TOL["dh0"] * want["dh0"].norm().item() + 1e-36
+    size = want["dg"].norm().item() + 1e-7 * want["dq"].norm().item()
+    assert (got["dg"].cpu().double() - want["dg"]).norm().item() <= 1e-3 * size
 
 
 def test_resets_inside_a_sequence(gdn):
