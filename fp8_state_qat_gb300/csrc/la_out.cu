@@ -23,6 +23,7 @@
 // weight the scores; four others write the outputs of the same item while the first go on to
 // the next. The roles of one chunk run next to each other and read the same tiles from L2.
 #include <algorithm>
+#include <cstddef>
 
 #include "la_chunk.cuh"
 #include "kernels.h"
@@ -31,11 +32,10 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kThreads = 384;            // warps 0 TMA, 1 products, 4-7 scores, 8-11 outputs
+constexpr int kThreads = 384;            // warps 0 TMA, 1 products, 2 gates, 4-7 scores, 8-11 outputs
 constexpr int kRing = 6;
 constexpr uint32_t TM_S = 0, TM_E = 128, TM_I = 256, TM_O = 384;   // scores (P in place), e c^T, state part, P c
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSmemBytes = kRing * kTile + 4 * 128 * 4 + 1024;
 constexpr int kSMs = 152;
 
 struct Params {
@@ -45,42 +45,58 @@ struct Params {
   int heads[4], width[4];   // of q, k, v, do
   int terms[2];
   int* status;
-  int64_t slots;
-  int roles, dk, dv;
+  int slots, roles, dk, dv;
 };
 struct Maps {
   CUtensorMap t[4];   // q, k, v, do
   CUtensorMap s[2];   // S, dS: rows of 64 value columns
 };
 
+// What the score and output warps need to know of an item, written by the gate warp.
+struct __align__(16) Entry {
+  int tok, L, h, role;         // L == 0: no more items
+  int pairwise;                // bit j: block j's decays are formed pair by pair (their range is too wide to factor)
+  int pad[3];
+  float tot[4];                // log-decay of a block
+  // per token of the chunk; "far" = towards the tokens that attend to it
+  float off[kC];               // decay from the token to the far edge of its block
+  float dcol[kC], drow[kC];    // factors of a block's own decays: exp(+-(gam - mid)), mid the middle of its range
+  float edge[kC];              // log-decay from the near edge of its block to the token
+  float st[kC];                // decay between the state and the token, times f_st
+  float hi[kC], lo[kC];        // prefix sums, for the pairwise decays
+};
+static_assert(offsetof(Entry, off) % 16 == 0 && offsetof(Entry, dcol) % 16 == 0, "read as float4");
+constexpr int kEntries = 2;
+constexpr uint32_t kSmemBytes = kRing * kTile + kEntries * sizeof(Entry) + 1024;
+static_assert(kSmemBytes <= 226 * 1024, "shared memory");
+
 struct Item {
-  int n, h, L, tok, role;
-  int64_t state;   // index among the states
+  int h, L, tok, role, state;   // state: index among the states
 };
 
 // The item's chunk, or false where no chunk uses its slot.
-__device__ __forceinline__ bool locate(const Params& p, int64_t i, Item& it) {
-  it.role = (int)(i % p.roles);
+__device__ __forceinline__ bool locate(const Params& p, int i, Item& it) {
+  it.role = i % p.roles;
   i /= p.roles;
-  it.h = (int)(i % p.gates.Hv);
-  const int64_t slot = i / p.gates.Hv;
+  it.state = i;
+  const int slot = i / p.gates.Hv;
+  it.h = i - slot * p.gates.Hv;
   int lo = 0, hi = p.seqs.N - 1;   // the last sequence whose slots start at or before this one
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (p.seqs.slot0(mid) <= slot) lo = mid;
+    if ((int)p.seqs.slot0(mid) <= slot) lo = mid;
     else hi = mid - 1;
   }
-  it.n = lo;
-  const int64_t t0 = p.seqs.start(lo), len = p.seqs.len(lo), c = slot - p.seqs.slot0(lo);
-  if (c < 0 || c * kC >= len) return false;
-  it.L = (int)(len - c * kC < kC ? len - c * kC : kC);
-  it.tok = (int)(t0 + c * kC);
-  it.state = slot * p.gates.Hv + it.h;
+  const int t0 = (int)p.seqs.start(lo), len = (int)p.seqs.len(lo), c = slot - (t0 / kC + lo);
+  if (c < 0 || c > (len - 1) / kC || len == 0) return false;
+  it.L = min(len - c * kC, kC);
+  it.tok = t0 + c * kC;
   return true;
 }
 
 struct Shared {
   uint64_t full[kRing], empty[kRing];
+  uint64_t gfull[kEntries], gempty[kEntries];
   uint64_t sc, oi, oo, pr, ofree;   // scores done, state part done, P c done, P written, accumulators read
   uint64_t drain;
   uint32_t tmem;
@@ -88,14 +104,25 @@ struct Shared {
 };
 
 // Bounded wait that also ends when another role has given up.
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity) {
-  const uint32_t a = tc::smem_u32(&bar);
+__device__ __noinline__ bool wait_slow(int* dead, uint32_t a, uint32_t parity) {
   for (uint32_t i = 0; i < GDN_WAIT_LIMIT; ++i) {
     if (tc::mbar_try_wait(a, parity)) return true;
-    if (*(volatile int*)&sh.dead) return false;
+    if (*(volatile int*)dead) return false;
   }
-  *(volatile int*)&sh.dead = 1;
+  *(volatile int*)dead = 1;
   return false;
+}
+__device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity) {
+  const uint32_t a = tc::smem_u32(&bar);
+  if (GDN_WAIT_LIMIT > 0 && tc::mbar_try_wait(a, parity)) return true;
+  return wait_slow(&sh.dead, a, parity);
+}
+
+// Four K = 16 steps of a product from shared memory, by one lane.
+__device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint32_t astep, uint64_t b, uint32_t bstep, uint32_t idesc,
+                                     bool first) {
+#pragma unroll
+  for (int s = 0; s < 4; ++s) tc::mma_bf16(d, dadv(a, s * astep), dadv(b, s * bstep), idesc, !first || s > 0);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -105,13 +132,18 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* const sm = smem_raw + (sbase - raw);
+  Entry* const entries = reinterpret_cast<Entry*>(sm + kRing * kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int64_t items = p.slots * p.gates.Hv * p.roles;
+  const int items = p.slots * p.gates.Hv * p.roles;
 
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.full[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh.empty[i]), 1);
+    }
+    for (int i = 0; i < kEntries; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.gfull[i]), 32);
+      tc::mbar_init(tc::smem_u32(&sh.gempty[i]), 1 + 128 + 128);
     }
     tc::mbar_init(tc::smem_u32(&sh.sc), 1);
     tc::mbar_init(tc::smem_u32(&sh.oi), 1);
@@ -129,289 +161,378 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
   const uint32_t tmem = sh.tmem;
   bool ok = true;
 
-  // Tiles of an item, in ring order: b, a, state (, c) -- with e: b, a, c, e, state hi, state lo.
+  // Tiles of an item, in ring order: b, a, state, c -- with e: b, a, c, e, state hi, state lo.
   if (tid == 0) {
-    uint32_t x = 0;   // tiles issued
-    auto slot_of = [&](uint32_t bytes) {
-      if (!ok) return sbase;
-      ok = wait(sh, sh.empty[x % kRing], ((x / kRing) & 1) ^ 1);
-      if (ok) tc::mbar_expect_tx(tc::smem_u32(&sh.full[x % kRing]), bytes);
-      return sbase + (x % kRing) * kTile;
+    uint32_t x = 0, slot = 0, turn = 0;   // tiles issued, x % kRing, (x / kRing) & 1
+    auto take_slot = [&](uint32_t bytes) {
+      if (!ok) return false;
+      ok = wait(sh, sh.empty[slot], turn ^ 1);
+      if (ok) tc::mbar_expect_tx(tc::smem_u32(&sh.full[slot]), bytes);
+      return ok;
     };
-    for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
+    auto next = [&] {
+      ++x;
+      if (++slot == kRing) {
+        slot = 0;
+        turn ^= 1;
+      }
+    };
+    for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
       Item it;
       if (!locate(p, i, it)) continue;
       const Role& r = p.role[it.role];
-      auto tokens = [&](int m) {
-        const int D = p.width[m], hh = it.h / (p.gates.Hv / p.heads[m]);
-        const uint32_t dst = slot_of(D / 64 * kBlk);
-        if (!ok) return;
-        for (int b = 0; b < D / 64; ++b)
-          tc::tma_load_3d(dst + b * kBlk, &maps.t[m], tc::smem_u32(&sh.full[x % kRing]), 64 * b, hh, it.tok);
-        ++x;
-      };
-      auto state = [&](int term) {
-        const uint32_t dst = slot_of(p.dk * p.dv * 2);
-        if (!ok) return;
-        const int64_t row = (it.state * p.terms[r.st] + term) * p.dk * (p.dv / 64);
-        for (int b = 0; b < p.dv / 64; ++b)
-          tc::tma_load_2d(dst + b * p.dk * 128, &maps.s[r.st], tc::smem_u32(&sh.full[x % kRing]), 0,
-                          (int)(row + b * p.dk));
-        ++x;
-      };
-      tokens(r.b);
-      tokens(r.a);
-      if (r.e >= 0) {
-        tokens(r.c);
-        tokens(r.e);
-        state(0);
-        state(1);
-      } else {
-        state(0);
-        tokens(r.c);
+      const int n = r.e >= 0 ? 6 : 4;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        // which tensor (0-3) or state term (4, 5) is tile j
+        const int m = j == 0 ? r.b : j == 1 ? r.a : n == 6 ? (j == 2 ? r.c : j == 3 ? r.e : j) : (j == 2 ? 4 : r.c);
+        if (m < 4) {
+          const int D = p.width[m], hh = it.h / (p.gates.Hv / p.heads[m]);
+          if (!take_slot(D / 64 * kBlk)) break;
+          const uint32_t dst = sbase + slot * kTile, bar = tc::smem_u32(&sh.full[slot]);
+          for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &maps.t[m], bar, 64 * b, hh, it.tok);
+        } else {
+          if (!take_slot(p.dk * p.dv * 2)) break;
+          const uint32_t dst = sbase + slot * kTile, bar = tc::smem_u32(&sh.full[slot]);
+          const int row = (it.state * p.terms[r.st] + (m - 4)) * p.dk * (p.dv / 64);
+          for (int b = 0; b < p.dv / 64; ++b)
+            tc::tma_load_2d(dst + b * p.dk * 128, &maps.s[r.st], bar, 0, row + b * p.dk);
+        }
+        next();
       }
     }
     // no copy may be in flight when the CTA ends
     for (uint32_t y = x > kRing ? x - kRing : 0; y < x; ++y)
       tc::mbar_wait(tc::smem_u32(&sh.full[y % kRing]), (y / kRing) & 1, 1u << 22);
-  } else if (tid == 32) {
-    uint32_t x = 0;
-    uint32_t k = 0;   // items done
+  } else if (warp == 2) {
+    // ---- gates: prefix sums and decay factors, one item ahead of the warps that use them ----
+    uint32_t k = 0;
+    int i = blockIdx.x;
+    Item it;
+    auto advance = [&] {
+      while (i < items && !locate(p, i, it)) i += gridDim.x;
+    };
+    advance();
+    float gx[4];
+    if (i < items) p.gates.load(gx, it.tok, it.h, it.L, lane);
+    while (true) {
+      const bool more = i < items;
+      const uint32_t s = k % kEntries;
+      ok = wait(sh, sh.gempty[s], ((k / kEntries) & 1) ^ 1);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      Entry& e = entries[s];
+      if (more) {
+        const Role& r = p.role[it.role];
+        const bool rev = r.reverse;
+        Gates g;
+        scan_gates(gx, g, lane);
+        if (lane == 0) {
+          e.tok = it.tok;
+          e.L = it.L;
+          e.h = it.h;
+          e.role = it.role;
+        }
+        int pairwise = 0;
+        float before = 0.f;   // log-decay from the state to the near edge of block j
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          // the blocks in order of their distance from the state; j is known at compile time in both orders
+          float sum = 0.f;
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+            if (rev ? m > jj : m < jj) sum += g.tot(m);
+          before = sum;
+          const int t = 32 * jj + lane;
+          const float pre = g.pre(jj), aft = g.after(jj);
+          float mx = pre, mn = pre;
+#pragma unroll
+          for (int off = 16; off > 0; off >>= 1) {
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+          }
+          // both factors stay within exp(+-32); their product is as exact as the prefix sums: while the
+          // range is 64, those of one float each
+          const float mid = 0.5f * (mx + mn);
+          if (!(mx - mn <= 64.f)) pairwise |= 1 << jj;
+          const float d = (g.hi[jj] - mid) + g.lo[jj];
+          const bool in = t < it.L;
+          e.off[t] = in ? expf(rev ? pre : aft) : 0.f;
+          e.drow[t] = expf(rev ? -d : d);
+          e.dcol[t] = expf(rev ? d : -d);
+          e.edge[t] = rev ? aft : pre;
+          e.st[t] = r.f_st * expf((rev ? aft : pre) + before);
+          e.hi[t] = g.hi[jj];
+          e.lo[t] = g.lo[jj];
+          if (lane == 0) e.tot[jj] = g.tot(jj);
+        }
+        if (lane == 0) e.pairwise = pairwise;
+        i += gridDim.x;
+        advance();
+        if (i < items) p.gates.load(gx, it.tok, it.h, it.L, lane);
+      } else if (lane == 0) {
+        e.L = 0;
+      }
+      tc::mbar_arrive(tc::smem_u32(&sh.gfull[s]));
+      ++k;
+      if (!more) break;
+    }
+  } else if (warp == 1) {
+    // ---- products: all lanes wait and compute descriptors, lane 0 issues ----
+    uint32_t x = 0, k = 0;
     auto tile = [&](uint32_t y) { return sbase + (y % kRing) * kTile; };
     auto landed = [&](uint32_t y) { ok = ok && wait(sh, sh.full[y % kRing], (y / kRing) & 1); };
     auto release = [&](uint32_t y) { tc::mma_commit(tc::smem_u32(&sh.empty[y % kRing])); };
-    for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-      Item it;
-      if (!locate(p, i, it)) continue;
-      const Role& r = p.role[it.role];
+    auto good = [&] { return ok = __all_sync(0xffffffffu, ok); };
+    while (true) {
+      const uint32_t gs = k % kEntries;
+      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      if (!good()) break;
+      const int role = entries[gs].role;
+      const bool more = entries[gs].L > 0;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
+      if (!more) break;
+      const Role& r = p.role[role];
       const bool dg = r.e >= 0;
-      const int da = p.width[r.a], dc = p.width[r.c];
+      const int na = p.width[r.a] / 64, nc = p.width[r.c] / 64;
       const uint32_t xb = x, xa = x + 1, xc = dg ? x + 2 : x + 3, xe = x + 3, xs = dg ? x + 4 : x + 2;
       // [128 x D] [128 x D]^T, both K-major
-      auto scores = [&](uint32_t d, uint32_t ta, uint32_t tb, int D) {
+      auto scores = [&](uint32_t d, uint32_t ta, uint32_t tb, int blocks) {
         const uint64_t ad = tc::make_sdesc(ta, 16, 1024), bd = tc::make_sdesc(tb, 16, 1024);
         constexpr uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 128, false, false);
-        for (int ks = 0; ks < D / 16; ++ks) {
-          const uint32_t at = (ks >> 2) * kBlk + (ks & 3) * 32;
-          tc::mma_bf16(tmem + d, dadv(ad, at), dadv(bd, at), idesc, ks > 0);
-        }
+#pragma unroll 1
+        for (int b = 0; b < blocks; ++b)
+          if (lane == 0) mma4(tmem + d, dadv(ad, b * kBlk), 32, dadv(bd, b * kBlk), 32, idesc, b == 0);
       };
       landed(xb);
       landed(xa);
       if (k > 0) ok = ok && wait(sh, sh.oo, (k - 1) & 1);   // P of the item before is consumed
-      if (!ok) break;
+      if (!good()) break;
       tc::tc_fence_after();
-      scores(TM_S, tile(xa), tile(xb), da);
-      release(xb);
+      scores(TM_S, tile(xa), tile(xb), na);
+      if (lane == 0) release(xb);
       if (dg) {
         landed(xc);
         landed(xe);
-        if (!ok) break;
-        scores(TM_E, tile(xe), tile(xc), dc);
+        if (!good()) break;
+        scores(TM_E, tile(xe), tile(xc), nc);
       }
-      tc::mma_commit(tc::smem_u32(&sh.sc));
+      if (lane == 0) tc::mma_commit(tc::smem_u32(&sh.sc));
       landed(xs);
       if (dg) landed(xs + 1);
       if (k > 0) ok = ok && wait(sh, sh.ofree, (k - 1) & 1);
-      if (!ok) break;
+      if (!good()) break;
       tc::tc_fence_after();
       // a St: St [da x dc] is stored as rows of the key channel, 64 value columns each
+      const uint32_t sblk = p.dk * 128;   // a block of 64 value columns
+      // transposed: K = value columns (K-major), N = key channels; else K = key channels, N = value columns (MN-major)
+      const uint32_t idesc_s = r.st_transposed ? tc::make_idesc(tc::kKindBF16, 128, p.dk, false, false)
+                                               : tc::make_idesc(tc::kKindBF16, 128, p.dv, false, true);
+      const uint32_t lbo = r.st_transposed ? 16 : sblk, kstep = r.st_transposed ? 32 : 2048;
+      const uint32_t kblk = r.st_transposed ? sblk : 8192;
+      const uint64_t ad = tc::make_sdesc(tile(xa), 16, 1024);
+#pragma unroll 1
       for (int t = 0; t < (dg ? 2 : 1); ++t) {
-        const uint64_t ad = tc::make_sdesc(tile(xa), 16, 1024);
-        const uint32_t sblk = p.dk * 128;   // a block of 64 value columns
-        if (r.st_transposed) {   // K = value columns (K-major), N = key channels
-          const uint64_t bd = tc::make_sdesc(tile(xs + t), 16, 1024);
-          const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, p.dk, false, false);
-          for (int ks = 0; ks < da / 16; ++ks)
-            tc::mma_bf16(tmem + TM_I, dadv(ad, (ks >> 2) * kBlk + (ks & 3) * 32),
-                         dadv(bd, (ks >> 2) * sblk + (ks & 3) * 32), idesc, t + ks > 0);
-        } else {                 // K = key channels, N = value columns (MN-major)
-          const uint64_t bd = tc::make_sdesc(tile(xs + t), sblk, 1024);
-          const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, p.dv, false, true);
-          for (int ks = 0; ks < da / 16; ++ks)
-            tc::mma_bf16(tmem + TM_I, dadv(ad, (ks >> 2) * kBlk + (ks & 3) * 32), dadv(bd, ks * 2048), idesc, t + ks > 0);
-        }
+        const uint64_t bd = tc::make_sdesc(tile(xs + t), lbo, 1024);
+#pragma unroll 1
+        for (int b = 0; b < na; ++b)
+          if (lane == 0) mma4(tmem + TM_I, dadv(ad, b * kBlk), 32, dadv(bd, b * kblk), kstep, idesc_s, t + b == 0);
       }
-      release(xa);
-      release(xs);
-      if (dg) release(xs + 1);
-      tc::mma_commit(tc::smem_u32(&sh.oi));
+      if (lane == 0) {
+        release(xa);
+        release(xs);
+        if (dg) release(xs + 1);
+        tc::mma_commit(tc::smem_u32(&sh.oi));
+      }
+      __syncwarp();
       landed(xc);
       ok = ok && wait(sh, sh.pr, k & 1);
-      if (!ok) break;
+      if (!good()) break;
       tc::tc_fence_after();
-      {
+      if (lane == 0) {
         const uint64_t bd = tc::make_sdesc(tile(xc), kBlk, 1024);
-        const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, dc, false, true);
+        const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 64 * nc, false, true);
+#pragma unroll
         for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks, dadv(bd, ks * 2048), idesc, ks > 0);
+        release(xc);
+        tc::mma_commit(tc::smem_u32(&sh.oo));
       }
-      release(xc);
-      tc::mma_commit(tc::smem_u32(&sh.oo));
+      __syncwarp();
       x += dg ? 6 : 4;
       ++k;
     }
     // the products in flight end before the tensor memory goes
     if (!ok) {
-      tc::mma_commit(tc::smem_u32(&sh.drain));
-      tc::mbar_wait(tc::smem_u32(&sh.drain), 0, 1u << 22);
+      if (lane == 0) {
+        tc::mma_commit(tc::smem_u32(&sh.drain));
+        tc::mbar_wait(tc::smem_u32(&sh.drain), 0, 1u << 22);
+      }
     } else if (k > 0) {
       ok = wait(sh, sh.oo, (k - 1) & 1);
     }
   } else if (warp >= 4 && warp < 8) {
+    // ---- scores -> weighted, masked, bf16 P; with e the pair sums of dg ----
     const int w = warp - 4;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
-    float* const col = reinterpret_cast<float*>(sm + kRing * kTile) + 128 * w;
     uint32_t x = 0, k = 0;
-    for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-      Item it;
-      if (!locate(p, i, it)) continue;
-      const Role& r = p.role[it.role];
+    while (true) {
+      const uint32_t gs = k % kEntries;
+      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Entry& e = entries[gs];
+      const int L = e.L;
+      if (L == 0) break;
+      const Role& r = p.role[e.role];
       const bool dg = r.e >= 0, rev = r.reverse;
-      const int dc = p.width[r.c];
-      const uint32_t xc = dg ? x + 2 : x + 3;
-      float gx[4];
-      Gates g;
-      p.gates.load(gx, it.tok, it.h, it.L, lane);
-      scan_gates(gx, g, lane);
-      // column factors: the decay from a token to the end of its block (or from the block's start to it)
-      __syncwarp();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) col[32 * j + lane] = 32 * j + lane < it.L ? expf(rev ? g.pre(j) : g.after(j)) : 0.f;
-      __syncwarp();
-      float ghi = 0.f, glo = 0.f, edge = 0.f;   // this row's prefix; the decay between it and its block's edge
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (j == w) {
-          ghi = g.hi[j];
-          glo = g.lo[j];
-          edge = rev ? g.after(j) : g.pre(j);
-        }
+      const float edge = e.edge[row], drow = e.drow[row];
+      const int pairwise = (e.pairwise >> w) & 1;
       ok = wait(sh, sh.sc, k & 1);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
-      float sum = 0.f;
-      uint32_t zero[16] = {};
-#pragma unroll
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
       for (int j = 0; j < 4; ++j) {
+        uint32_t u[16];
         if (rev ? j < w : j > w) {
-          tmem_st16u(tc::tmem_addr(tmem, lane0, TM_S + 16 * j), zero);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) u[c] = 0;
+          tmem_st16u(tc::tmem_addr(tmem, lane0, TM_S + 16 * j), u);
           continue;
         }
+        const bool diag = j == w;
+        // columns of this block that the row takes: tokens past the chunk's end may hold anything
+        uint32_t mask = 0xffffffffu;
+        if (rev && L - 32 * j < 32) mask = L > 32 * j ? (1u << (L - 32 * j)) - 1u : 0u;
+        if (diag) mask &= rev ? 0xffffffffu << lane : 0xffffffffu >> (31 - lane);
+        float f = drow;
+        if (!diag) {   // from this row to the block's near edge
+          float z = edge;
+#pragma unroll
+          for (int m = 1; m < 3; ++m)
+            if (rev ? (m > w && m < j) : (m > j && m < w)) z += e.tot[m];
+          f = expf(z);
+        }
+        const float* cf = (diag ? e.dcol : e.off) + 32 * j;
         float v[32];
         ld32(tmem, lane0, TM_S + 32 * j, v);
-        if (j == w) {
+        if (diag && pairwise) {
+          const float hr = e.hi[row], lr = e.lo[row];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float ch = __shfl_sync(0xffffffffu, ghi, c), cl = __shfl_sync(0xffffffffu, glo, c);
-            const float d = (ghi - ch) + (glo - cl);
-            const bool in = rev ? (c >= lane && 32 * j + c < it.L) : c <= lane;
-            v[c] = in ? v[c] * __expf(rev ? -d : d) : 0.f;
+            const float d = (hr - e.hi[32 * j + c]) + (lr - e.lo[32 * j + c]);
+            v[c] = (mask >> c) & 1 ? v[c] * __expf(rev ? -d : d) : 0.f;
           }
         } else {
-          float e = edge;
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if (rev ? (m > w && m < j) : (m > j && m < w)) e += g.tot(m);
-          const float f = expf(e);
+          const float2 f2 = make_float2(f, f);
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
-            const float4 cf = *reinterpret_cast<const float4*>(col + 32 * j + c);
-            const float cc[4] = {cf.x, cf.y, cf.z, cf.w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q)   // tokens past the chunk's end may hold anything
-              v[c + q] = !rev || 32 * j + c + q < it.L ? v[c + q] * (f * cc[q]) : 0.f;
+            const float4 cc = *reinterpret_cast<const float4*>(cf + c);
+            const float2 a = __fmul2_rn(make_float2(v[c], v[c + 1]), __fmul2_rn(f2, make_float2(cc.x, cc.y)));
+            const float2 b = __fmul2_rn(make_float2(v[c + 2], v[c + 3]), __fmul2_rn(f2, make_float2(cc.z, cc.w)));
+            v[c] = (mask >> c) & 1 ? a.x : 0.f;
+            v[c + 1] = (mask >> (c + 1)) & 1 ? a.y : 0.f;
+            v[c + 2] = (mask >> (c + 2)) & 1 ? b.x : 0.f;
+            v[c + 3] = (mask >> (c + 3)) & 1 ? b.y : 0.f;
           }
         }
-        if (dg) {
-          float ev[32];
-          ld32(tmem, lane0, TM_E + 32 * j, ev);
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            const bool in = j == w ? (rev ? (c > lane && 32 * j + c < it.L) : c < lane) : (!rev || 32 * j + c < it.L);
-            sum += in ? v[c] * ev[c] : 0.f;
-          }
-        }
-        uint32_t u[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) u[c] = pack_bf16(v[2 * c], v[2 * c + 1]);
         // columns [16 j, 16 j + 16) hold scores of blocks <= j / 2, read before
         tmem_st16u(tc::tmem_addr(tmem, lane0, TM_S + 16 * j), u);
+        if (dg) {
+          if (diag) mask &= ~(1u << lane);   // pairs of different tokens
+          float ev[32];
+          ld32(tmem, lane0, TM_E + 32 * j, ev);
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            ev[c] = (mask >> c) & 1 ? ev[c] : 0.f;
+            ev[c + 1] = (mask >> (c + 1)) & 1 ? ev[c + 1] : 0.f;
+            sum = __ffma2_rn(make_float2(v[c], v[c + 1]), make_float2(ev[c], ev[c + 1]), sum);
+          }
+        }
       }
       tc::tmem_st_wait();
-      if (it.L < kC) {   // rows past the end of c would meet zero weights: not with a NaN
+      const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
+      if (L < kC) {   // rows past the end of c would meet zero weights: not with a NaN
+        const uint32_t xc = dg ? x + 2 : x + 3;
         ok = wait(sh, sh.full[xc % kRing], (xc / kRing) & 1);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        zero_tail_rows(sm + (xc % kRing) * kTile, dc / 64, tid - 128, it.L);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        zero_tail_rows(sm + (xc % kRing) * kTile, p.width[r.c] / 64, tid - 128, L);
         tc::fence_proxy_async_smem();
       }
       tc::tc_fence_before();
       tc::mbar_arrive(tc::smem_u32(&sh.pr));
-      if (dg && row < it.L) r.dot_in[(int64_t)(it.tok + row) * p.gates.Hv + it.h] = r.f_in * sum;
+      tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
+      if (dg && row < L) r.dot_in[at] = r.f_in * (sum.x + sum.y);
       x += dg ? 6 : 4;
       ++k;
     }
   } else if (warp >= 8) {
+    // ---- outputs ----
     const int w = warp - 8;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
     uint32_t x = 0, k = 0;
-    for (int64_t i = blockIdx.x; i < items && ok; i += gridDim.x) {
-      Item it;
-      if (!locate(p, i, it)) continue;
-      const Role& r = p.role[it.role];
-      const bool dg = r.e >= 0, rev = r.reverse;
-      const int dc = p.width[r.c];
-      float gx[4];
-      Gates g;
-      p.gates.load(gx, it.tok, it.h, it.L, lane);
-      scan_gates(gx, g, lane);
-      float e = 0.f;   // log of the decay between the state and this row
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (j == w) e += rev ? g.after(j) : g.pre(j);
-        if (rev ? j > w : j < w) e += g.tot(j);
-      }
-      const float fs = expf(e) * r.f_st, fi = r.f_in;
-      const int64_t at = (int64_t)(it.tok + row) * p.gates.Hv + it.h;
+    while (true) {
+      const uint32_t gs = k % kEntries;
+      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const Entry& e = entries[gs];
+      const int L = e.L;
+      if (L == 0) break;
+      const Role& r = p.role[e.role];
+      const bool dg = r.e >= 0;
+      const int nb = p.width[r.c] / 32;
+      const float fs = e.st[row], fi = r.f_in;
+      const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
+      tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
       ok = wait(sh, sh.oi, k & 1);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       if (dg) {
         const uint32_t xe = x + 3;
         ok = wait(sh, sh.full[xe % kRing], (xe / kRing) & 1);   // landed long ago; makes it visible here
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const unsigned char* et = sm + (xe % kRing) * kTile;
-        float dot = 0.f;
-        for (int b = 0; b < dc / 32; ++b) {
+        float2 dot[2] = {};
+#pragma unroll 1
+        for (int b = 0; b < nb; ++b) {
           float v[32];
           ld32(tmem, lane0, TM_I + 32 * b, v);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            float ev[8];
-            load_bf16x8(reinterpret_cast<const __nv_bfloat16*>(et + (b >> 1) * kBlk + tc::sw128(row, 64 * (b & 1) + 16 * c)), ev);
+            const uint4 q = *reinterpret_cast<const uint4*>(et + (b >> 1) * kBlk + tc::sw128(row, 64 * (b & 1) + 16 * c));
+            const uint32_t u[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int q = 0; q < 8; ++q) dot = fmaf(ev[q], v[8 * c + q], dot);
+            for (int h = 0; h < 4; ++h)
+              dot[h & 1] = __ffma2_rn(unpack_bf16(u[h]), make_float2(v[8 * c + 2 * h], v[8 * c + 2 * h + 1]), dot[h & 1]);
           }
         }
-        if (row < it.L) r.dot_st[at] = fs * dot;
+        if (row < L) r.dot_st[at] = fs * ((dot[0].x + dot[0].y) + (dot[1].x + dot[1].y));
       }
       ok = wait(sh, sh.oo, k & 1);
-      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
-      for (int b = 0; b < dc / 32; ++b) {
+      const float2 fs2 = make_float2(fs, fs), fi2 = make_float2(fi, fi);
+#pragma unroll 1
+      for (int b = 0; b < nb; ++b) {
         float v[32], s[32];
         ld32(tmem, lane0, TM_O + 32 * b, v);
         ld32(tmem, lane0, TM_I + 32 * b, s);
 #pragma unroll
-        for (int c = 0; c < 32; ++c) v[c] = fmaf(fs, s[c], fi * v[c]);
-        if (row < it.L) {
+        for (int c = 0; c < 32; c += 2) {
+          const float2 o = __ffma2_rn(fs2, make_float2(s[c], s[c + 1]), __fmul2_rn(fi2, make_float2(v[c], v[c + 1])));
+          v[c] = o.x;
+          v[c + 1] = o.y;
+        }
+        if (row < L) {
           if (r.out_f32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at * dc + 32 * b);
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at * (32 * nb) + 32 * b);
 #pragma unroll
             for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
           } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) + at * dc + 32 * b);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) + at * (32 * nb) + 32 * b);
 #pragma unroll
             for (int c = 0; c < 4; ++c) dst[c] = pack8(v + 8 * c);
           }
@@ -441,12 +562,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
 }  // namespace
 
 cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cudaStream_t stream) {
-  const int64_t tokens = (int64_t)p.B * p.T, slots = la_slots(p), items = slots * p.Hv * r.roles;
+  const int64_t tokens = (int64_t)p.B * p.T, slots = la_slots(p), items = slots * p.Hv * r.roles;   // < 2^24
   if (tokens == 0 || items == 0) return cudaSuccess;
   Maps m;
   const void* base[4] = {r.q, r.k, r.v, r.dout};
   Params o{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, {}, {p.Hqk, p.Hqk, p.Hv, p.Hv}, {p.dk, p.dk, p.dv, p.dv},
-           {r.terms[0], r.terms[1]}, status, slots, r.roles, p.dk, p.dv};
+           {r.terms[0], r.terms[1]}, status, (int)slots, r.roles, p.dk, p.dv};
   for (int i = 0; i < r.roles; ++i) o.role[i] = r.role[i];
   for (int i = 0; i < 4; ++i)
     if (!make_bf16_map(&m.t[i], base[i] ? base[i] : r.q, o.width[i], o.heads[i], tokens, kC)) return cudaErrorNotSupported;
