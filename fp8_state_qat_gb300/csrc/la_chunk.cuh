@@ -99,6 +99,21 @@ __device__ __forceinline__ void zero_tail_rows(unsigned char* tile, int blocks, 
   }
 }
 
+// Bounded wait that also ends when another warp has given up (`dead`, in shared memory).
+static __device__ __noinline__ bool wait_slow(int* dead, uint32_t a, uint32_t parity) {
+  for (uint32_t i = 0; i < GDN_WAIT_LIMIT; ++i) {
+    if (tc::mbar_try_wait(a, parity)) return true;
+    if (*(volatile int*)dead) return false;
+  }
+  *(volatile int*)dead = 1;
+  return false;
+}
+__device__ __forceinline__ bool wait(int& dead, uint64_t& bar, uint32_t parity) {
+  const uint32_t a = tc::smem_u32(&bar);
+  if (GDN_WAIT_LIMIT > 0 && tc::mbar_try_wait(a, parity)) return true;
+  return wait_slow(&dead, a, parity);
+}
+
 // ---- launchers of the parts (la_state.cu, la_out.cu) ----
 // States at chunk boundaries, bf16 terms per item = slot * Hv + h: [term][dv / 64][dk][64].
 struct StateRun {

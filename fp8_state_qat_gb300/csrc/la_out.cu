@@ -98,25 +98,11 @@ struct Shared {
   uint64_t full[kRing], empty[kRing];
   uint64_t gfull[kEntries], gempty[kEntries];
   uint64_t sc, oi, oo, pr, ofree;   // scores done, state part done, P c done, P written, accumulators read
+  uint64_t eread;                    // e read by every output thread
   uint64_t drain;
   uint32_t tmem;
   int dead;                          // a wait gave up: every role winds down
 };
-
-// Bounded wait that also ends when another role has given up.
-__device__ __noinline__ bool wait_slow(int* dead, uint32_t a, uint32_t parity) {
-  for (uint32_t i = 0; i < GDN_WAIT_LIMIT; ++i) {
-    if (tc::mbar_try_wait(a, parity)) return true;
-    if (*(volatile int*)dead) return false;
-  }
-  *(volatile int*)dead = 1;
-  return false;
-}
-__device__ __forceinline__ bool wait(Shared& sh, uint64_t& bar, uint32_t parity) {
-  const uint32_t a = tc::smem_u32(&bar);
-  if (GDN_WAIT_LIMIT > 0 && tc::mbar_try_wait(a, parity)) return true;
-  return wait_slow(&sh.dead, a, parity);
-}
 
 // Four K = 16 steps of a product from shared memory, by one lane.
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint32_t astep, uint64_t b, uint32_t bstep, uint32_t idesc,
@@ -151,6 +137,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     tc::mbar_init(tc::smem_u32(&sh.drain), 1);
     tc::mbar_init(tc::smem_u32(&sh.pr), 128);
     tc::mbar_init(tc::smem_u32(&sh.ofree), 128);
+    tc::mbar_init(tc::smem_u32(&sh.eread), 128);
     tc::mbar_fence_init();
     sh.dead = 0;
   }
@@ -166,7 +153,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     uint32_t x = 0, slot = 0, turn = 0;   // tiles issued, x % kRing, (x / kRing) & 1
     auto take_slot = [&](uint32_t bytes) {
       if (!ok) return false;
-      ok = wait(sh, sh.empty[slot], turn ^ 1);
+      ok = wait(sh.dead, sh.empty[slot], turn ^ 1);
       if (ok) tc::mbar_expect_tx(tc::smem_u32(&sh.full[slot]), bytes);
       return ok;
     };
@@ -218,7 +205,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     while (true) {
       const bool more = i < items;
       const uint32_t s = k % kEntries;
-      ok = wait(sh, sh.gempty[s], ((k / kEntries) & 1) ^ 1);
+      ok = wait(sh.dead, sh.gempty[s], ((k / kEntries) & 1) ^ 1);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       Entry& e = entries[s];
       if (more) {
@@ -280,12 +267,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     // ---- products: all lanes wait and compute descriptors, lane 0 issues ----
     uint32_t x = 0, k = 0;
     auto tile = [&](uint32_t y) { return sbase + (y % kRing) * kTile; };
-    auto landed = [&](uint32_t y) { ok = ok && wait(sh, sh.full[y % kRing], (y / kRing) & 1); };
+    auto landed = [&](uint32_t y) { ok = ok && wait(sh.dead, sh.full[y % kRing], (y / kRing) & 1); };
     auto release = [&](uint32_t y) { tc::mma_commit(tc::smem_u32(&sh.empty[y % kRing])); };
     auto good = [&] { return ok = __all_sync(0xffffffffu, ok); };
     while (true) {
       const uint32_t gs = k % kEntries;
-      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      ok = wait(sh.dead, sh.gfull[gs], (k / kEntries) & 1);
       if (!good()) break;
       const int role = entries[gs].role;
       const bool more = entries[gs].L > 0;
@@ -306,7 +293,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       };
       landed(xb);
       landed(xa);
-      if (k > 0) ok = ok && wait(sh, sh.oo, (k - 1) & 1);   // P of the item before is consumed
+      if (k > 0) ok = ok && wait(sh.dead, sh.oo, (k - 1) & 1);   // P of the item before is consumed
       if (!good()) break;
       tc::tc_fence_after();
       scores(TM_S, tile(xa), tile(xb), na);
@@ -320,7 +307,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (lane == 0) tc::mma_commit(tc::smem_u32(&sh.sc));
       landed(xs);
       if (dg) landed(xs + 1);
-      if (k > 0) ok = ok && wait(sh, sh.ofree, (k - 1) & 1);
+      if (k > 0) ok = ok && wait(sh.dead, sh.ofree, (k - 1) & 1);
       if (!good()) break;
       tc::tc_fence_after();
       // a St: St [da x dc] is stored as rows of the key channel, 64 value columns each
@@ -346,7 +333,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       }
       __syncwarp();
       landed(xc);
-      ok = ok && wait(sh, sh.pr, k & 1);
+      ok = ok && wait(sh.dead, sh.pr, k & 1);
       if (!good()) break;
       tc::tc_fence_after();
       if (lane == 0) {
@@ -368,7 +355,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         tc::mbar_wait(tc::smem_u32(&sh.drain), 0, 1u << 22);
       }
     } else if (k > 0) {
-      ok = wait(sh, sh.oo, (k - 1) & 1);
+      ok = wait(sh.dead, sh.oo, (k - 1) & 1);
     }
   } else if (warp >= 4 && warp < 8) {
     // ---- scores -> weighted, masked, bf16 P; with e the pair sums of dg ----
@@ -378,7 +365,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     uint32_t x = 0, k = 0;
     while (true) {
       const uint32_t gs = k % kEntries;
-      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      ok = wait(sh.dead, sh.gfull[gs], (k / kEntries) & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const Entry& e = entries[gs];
       const int L = e.L;
@@ -387,7 +374,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       const bool dg = r.e >= 0, rev = r.reverse;
       const float edge = e.edge[row], drow = e.drow[row];
       const int pairwise = (e.pairwise >> w) & 1;
-      ok = wait(sh, sh.sc, k & 1);
+      ok = wait(sh.dead, sh.sc, k & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       float2 sum = make_float2(0.f, 0.f);
@@ -456,7 +443,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
       if (L < kC) {   // rows past the end of c would meet zero weights: not with a NaN
         const uint32_t xc = dg ? x + 2 : x + 3;
-        ok = wait(sh, sh.full[xc % kRing], (xc / kRing) & 1);
+        ok = wait(sh.dead, sh.full[xc % kRing], (xc / kRing) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         zero_tail_rows(sm + (xc % kRing) * kTile, p.width[r.c] / 64, tid - 128, L);
         tc::fence_proxy_async_smem();
@@ -473,10 +460,10 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     const int w = warp - 8;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
-    uint32_t x = 0, k = 0;
+    uint32_t x = 0, k = 0, dgs = 0;
     while (true) {
       const uint32_t gs = k % kEntries;
-      ok = wait(sh, sh.gfull[gs], (k / kEntries) & 1);
+      ok = wait(sh.dead, sh.gfull[gs], (k / kEntries) & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const Entry& e = entries[gs];
       const int L = e.L;
@@ -487,12 +474,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       const float fs = e.st[row], fi = r.f_in;
       const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
       tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
-      ok = wait(sh, sh.oi, k & 1);
+      ok = wait(sh.dead, sh.oi, k & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       if (dg) {
         const uint32_t xe = x + 3;
-        ok = wait(sh, sh.full[xe % kRing], (xe / kRing) & 1);   // landed long ago; makes it visible here
+        ok = wait(sh.dead, sh.full[xe % kRing], (xe / kRing) & 1);   // landed long ago; makes it visible here
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         const unsigned char* et = sm + (xe % kRing) * kTile;
         float2 dot[2] = {};
@@ -511,7 +498,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         }
         if (row < L) r.dot_st[at] = fs * ((dot[0].x + dot[0].y) + (dot[1].x + dot[1].y));
       }
-      ok = wait(sh, sh.oo, k & 1);
+      ok = wait(sh.dead, sh.oo, k & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       const float2 fs2 = make_float2(fs, fs), fi2 = make_float2(fi, fi);
@@ -540,9 +527,14 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       }
       tc::tc_fence_before();
       tc::mbar_arrive(tc::smem_u32(&sh.ofree));
-      if (dg) {   // e is read by all four warps
-        tc::named_bar_sync(1, 128);
-        if (tid == 256) tc::mbar_arrive(tc::smem_u32(&sh.empty[(x + 3) % kRing]));
+      if (dg) {   // all four warps read e; its slot is free when the last has
+        tc::mbar_arrive(tc::smem_u32(&sh.eread));
+        if (w == 0) {
+          ok = wait(sh.dead, sh.eread, dgs & 1);
+          if (!(ok = __all_sync(0xffffffffu, ok))) break;
+          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.empty[(x + 3) % kRing]));
+        }
+        ++dgs;
       }
       x += dg ? 6 : 4;
       ++k;

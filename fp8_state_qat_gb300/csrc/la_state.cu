@@ -9,8 +9,9 @@
 // a fresh accumulator, and the walk itself is one fp32 multiply-add per state element, held in
 // registers. The weights go to the K side, as the A operand in tensor memory: thread = key channel
 // reads its column of the K tile, and w_i k_i (fp32) is written as three bf16 terms (24 bits, so the
-// state has fp32 accuracy; two terms leave 2^-17 of it), A terms of chunk c + 1 being written while the
-// products of chunk c run. V stays as TMA left it (MN-major B operand).
+// state has fp32 accuracy; two terms leave 2^-17 of it), the A terms of chunk c + 1 while the products of
+// chunk c run. That splitting is what the kernel spends its time on (about 7 instructions per K element and
+// value tile), so 16 warps do it. V stays as TMA left it (MN-major B operand).
 // Tail rows of a partial chunk belong to another sequence, so they are zeroed, not just weighted by zero.
 //
 // Few sequences and heads: each walk is cut into segments, a first launch computes every segment's
@@ -25,7 +26,7 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kWorkers = 512, kThreads = kWorkers + 32;
 constexpr int kStages = 3;
 constexpr uint32_t TM_A = 0, TM_ACC = 384;   // two buffers of three 64-column A terms; the accumulator
 constexpr uint32_t kTmemCols = 512;
@@ -46,213 +47,247 @@ struct Params {
 template <int NV>
 constexpr uint32_t stage_bytes() { return kTile + NV / 64 * kBlk; }
 template <int NV>
-constexpr uint32_t smem_bytes() { return kStages * stage_bytes<NV>() + 8 * 64 * 4 + 1024; }
+constexpr uint32_t smem_bytes() { return kStages * stage_bytes<NV>() + 1024; }
 
+struct Shared {
+  uint64_t full[kStages];   // a step's tiles have landed
+  uint64_t wready[2];       // its weights are written
+  uint64_t aready;          // its A terms are written and the accumulator of the step before is read
+  uint64_t mma;             // its product is complete
+  uint32_t tmem;
+  int dead;
+  float decay[2];
+  float w[2][kC];
+};
+
+// Warps 0-15 weight K and hold the state; warp 16 loads, computes the weights and issues the products.
 template <int NV>
 __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty, const Params p) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[kStages + 1];
-  __shared__ uint32_t tmem_slot;
-  constexpr int HC = NV / 2;   // value columns a thread
+  __shared__ __align__(16) Shared sh;
+  constexpr int HC = NV / 4;   // value columns a thread
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (sbase - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = warp & 3, half = warp >> 2;
+  const int quad = warp & 3, part = warp >> 2;
   const uint32_t lane0 = 32u * quad;
   const int row = 32 * quad + lane;        // key channel
   const bool live = row < p.dk;            // dk 64: lanes 64-127 of the product are not used
-  float* const ws = reinterpret_cast<float*>(sm + kStages * stage_bytes<NV>()) + warp * 64;
 
   const int tiles = p.dv / NV;
-  int64_t u = blockIdx.x;
-  const int vt = (int)(u % tiles);
+  int u = blockIdx.x;
+  const int vt = u % tiles;
   u /= tiles;
-  const int seg = (int)(u % p.nseg);
-  const int64_t unit = u / p.nseg;
+  const int seg = u % p.nseg;
+  const int unit = u / p.nseg;
   if (p.totals && seg == p.nseg - 1) return;   // nothing follows the last segment
   const int Hv = p.gates.Hv;
-  const int n = (int)(unit / Hv), h = (int)(unit % Hv), hq = h / (Hv / p.Hqk);
-  const int64_t t0 = p.seqs.start(n), len = p.seqs.len(n), slot0 = p.seqs.slot0(n);
-  const int nch = (int)((len + kC - 1) / kC);
+  const int n = unit / Hv, h = unit % Hv, hq = h / (Hv / p.Hqk);
+  const int t0 = (int)p.seqs.start(n), len = (int)p.seqs.len(n), slot0 = (int)p.seqs.slot0(n);
+  const int nch = len / kC + (len % kC != 0);
   const int per = (nch + p.nseg - 1) / p.nseg;
   const int first = min(seg * per, nch), last = min(first + per, nch);   // walk steps of this CTA
   const int steps = last - first;
   auto chunk_of = [&](int i) { return p.reverse ? nch - 1 - (first + i) : first + i; };
-  auto rows_of = [&](int c) { return (int)min((int64_t)kC, len - (int64_t)c * kC); };
+  auto rows_of = [&](int c) { return min(kC, len - c * kC); };
 
-  const uint32_t bar_m = tc::smem_u32(&bars[kStages]);
-  const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, NV, false, true);
-  auto load = [&](int i) {
-    const uint32_t bar = tc::smem_u32(&bars[i % kStages]), dst = sbase + (i % kStages) * stage_bytes<NV>();
-    const int tok = (int)(t0 + (int64_t)chunk_of(i) * kC);
-    tc::mbar_expect_tx(bar, p.dk / 64 * kBlk + NV / 64 * kBlk);
-    for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, tok);
-    for (int b = 0; b < NV / 64; ++b) tc::tma_load_3d(dst + kTile + b * kBlk, &ty, bar, vt * NV + 64 * b, h, tok);
-  };
   if (tid == 0) {
-    for (int i = 0; i <= kStages; ++i) tc::mbar_init(tc::smem_u32(&bars[i]), 1);
+    for (int i = 0; i < kStages; ++i) tc::mbar_init(tc::smem_u32(&sh.full[i]), 1);
+    for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
+    tc::mbar_init(tc::smem_u32(&sh.aready), kWorkers / 32);
+    tc::mbar_init(tc::smem_u32(&sh.mma), 1);
     tc::mbar_fence_init();
-    for (int i = 0; i < min(2, steps); ++i) load(i);
+    sh.dead = 0;
   }
-  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&tmem_slot), kTmemCols);
-  float gx[4];
-  if (steps) p.gates.load(gx, t0 + (int64_t)chunk_of(0) * kC, h, rows_of(chunk_of(0)), lane);
+  if (warp == 0) tc::tmem_alloc(tc::smem_u32(&sh.tmem), kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  bool ok = true;
 
-  // state elements (row, vt NV + half HC + j)
-  float s[HC];
-  const int64_t sbase_g = (unit * p.dk + row) * (int64_t)p.dv + vt * NV + half * HC;
-  const int64_t seg_g = ((unit * p.nseg + seg) * p.dk + row) * (int64_t)p.dv + vt * NV + half * HC;
-  {
+  float s[HC];   // state elements (row, vt NV + part HC + j)
+  const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * NV + part * HC;
+  const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * NV + part * HC;
+  float log_decay = 0.f;   // of the whole segment (warp 16)
+
+  if (warp == kWorkers / 32) {
+    const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, NV, false, true);
+    int loaded = 0;
+    auto load = [&](int i) {
+      const uint32_t bar = tc::smem_u32(&sh.full[i % kStages]), dst = sbase + (i % kStages) * stage_bytes<NV>();
+      const int tok = t0 + chunk_of(i) * kC;
+      tc::mbar_expect_tx(bar, p.dk / 64 * kBlk + NV / 64 * kBlk);
+      for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, tok);
+      for (int b = 0; b < NV / 64; ++b) tc::tma_load_3d(dst + kTile + b * kBlk, &ty, bar, vt * NV + 64 * b, h, tok);
+    };
+    if (lane == 0)
+      for (; loaded < min(2, steps); ++loaded) load(loaded);
+    float gx[4];
+    auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
+    auto weights = [&](int i) {   // of step i, from gx
+      const int L = rows_of(chunk_of(i));
+      Gates w;
+      scan_gates(gx, w, lane);
+      if (i + 1 < steps) gates(i + 1);
+      const float tt[4] = {w.tot(0), w.tot(1), w.tot(2), w.tot(3)};
+      const float all = (tt[0] + tt[1]) + (tt[2] + tt[3]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float e = p.reverse ? w.pre(q) : w.after(q);
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          if (p.reverse ? m < q : m > q) e += tt[m];
+        sh.w[i & 1][32 * q + lane] = 32 * q + lane < L ? p.scale * expf(e) : 0.f;
+      }
+      if (lane == 0) sh.decay[i & 1] = expf(all);
+      log_decay += all;
+      tc::mbar_arrive(tc::smem_u32(&sh.wready[i & 1]));
+    };
+    if (steps) {
+      gates(0);
+      weights(0);
+    }
+    int issued = 0;
+    for (int i = 0; i < steps; ++i) {
+      if (i + 1 < steps) weights(i + 1);   // the workers are past step i - 1, whose weights lie there
+      ok = wait(sh.dead, sh.aready, i & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::tc_fence_after();
+      if (lane == 0) {
+        const uint64_t bd = tc::make_sdesc(sbase + (i % kStages) * stage_bytes<NV>() + kTile, kBlk, 1024);
+        const uint32_t a = tmem + TM_A + (i & 1) * 192;
+#pragma unroll
+        for (int t = 0; t < 3; ++t)
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ta(tmem + TM_ACC, a + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc, t + ks > 0);
+        tc::mma_commit(tc::smem_u32(&sh.mma));
+        if (i + 2 < steps) {   // its stage held step i - 1, whose product the workers have taken
+          load(i + 2);
+          ++loaded;
+        }
+      }
+      __syncwarp();
+      issued = i + 1;
+    }
+    if (lane == 0 && !ok) {   // nothing of this CTA is in flight when it ends
+      for (int i = max(0, loaded - kStages); i < loaded; ++i)
+        tc::mbar_wait(tc::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, 1u << 22);
+      if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma), (issued - 1) & 1, 1u << 22);
+    }
+  } else {
     const float* src = p.totals ? nullptr : p.nseg > 1 ? p.seg_tot + seg_g : p.s0 ? p.s0 + sbase_g : nullptr;
 #pragma unroll
     for (int j = 0; j < HC; j += 4) {
       const float4 v = src && live ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
       s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
     }
-  }
-  tc::tc_fence_before();
-  __syncthreads();
-  tc::tc_fence_after();
-  const uint32_t tmem = tmem_slot;
-  // byte offsets of this channel within an 8-row group of the swizzled tile
-  uint32_t off[8];
+    // byte offsets of this channel within an 8-row group of the swizzled tile
+    uint32_t off[8];
 #pragma unroll
-  for (int r = 0; r < 8; ++r) off[r] = (row >> 6) * kBlk + tc::sw128(r, (row & 63) * 2);
-
-  bool ok = true;
-  int loaded = min(2, steps), waited = 0;   // TMA stages issued / seen complete (thread 0 drains the rest)
-  int mma_issued = 0;
-  float decay = 1.f;                        // Gam of the chunk whose product is in flight
-  float log_decay = 0.f;                    // of the whole segment
-  auto take = [&](int i) {                  // the product of step i -> the state
-    ok = ok && tc::mbar_wait(bar_m, i & 1);
-    tc::tc_fence_after();
-    if (live || p.dk == 128) {
+    for (int r = 0; r < 8; ++r) off[r] = (row >> 6) * kBlk + part * 4096 + tc::sw128(r, (row & 63) * 2);
+    const bool work = 32 * quad < p.dk;   // uniform in the warp
+    float decay = 1.f;                    // Gam of the chunk whose product is in flight
+    auto take = [&](int i) {              // the product of step i -> the state
+      ok = wait(sh.dead, sh.mma, i & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      tc::tc_fence_after();
+      if (!work) return;
+      float v[HC];
 #pragma unroll
-      for (int q = 0; q < HC / 32; ++q) {
-        float v[32];
-        ld32(tmem, lane0, TM_ACC + half * HC + 32 * q, v);
+      for (int q = 0; q < HC; q += 16) tc::tmem_ld16(tc::tmem_addr(tmem, lane0, TM_ACC + part * HC + q), v + q);
+      tc::tmem_ld_wait();
+      const float2 d2 = make_float2(decay, decay);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) s[32 * q + j] = fmaf(decay, s[32 * q + j], v[j]);
+      for (int j = 0; j < HC; j += 2) {
+        const float2 r = __ffma2_rn(d2, make_float2(s[j], s[j + 1]), make_float2(v[j], v[j + 1]));
+        s[j] = r.x;
+        s[j + 1] = r.y;
       }
-    }
-    tc::tc_fence_before();
-  };
-
-  for (int i = 0; i < steps; ++i) {
-    const int c = chunk_of(i), L = rows_of(c);
-    unsigned char* kt = sm + (i % kStages) * stage_bytes<NV>();
-    Gates w;
-    scan_gates(gx, w, lane);
-    if (i + 1 < steps) {
-      const int c1 = chunk_of(i + 1);
-      p.gates.load(gx, t0 + (int64_t)c1 * kC, h, rows_of(c1), lane);
-    }
-    // this warp's 64 weights (tokens 64 half ..) to shared memory
-    const float tt[4] = {w.tot(0), w.tot(1), w.tot(2), w.tot(3)};
+    };
+    const float2 neg = make_float2(-1.f, -1.f);
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      const int c = chunk_of(i), L = rows_of(c);
+      unsigned char* kt = sm + (i % kStages) * stage_bytes<NV>();
+      ok = wait(sh.dead, sh.full[i % kStages], (i / kStages) & 1) && wait(sh.dead, sh.wready[i & 1], (i >> 1) & 1);
+      if (L < kC) {   // uniform: the tail rows are another sequence's. K: what this warp reads; V: the product
+        const int r = 32 * part + lane;
+        if (r >= L) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      if ((q >> 1) != half) continue;
-      float e = p.reverse ? w.pre(q) : w.after(q);
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        if (p.reverse ? m < q : m > q) e += tt[m];
-      __syncwarp();
-      ws[32 * (q & 1) + lane] = 32 * q + lane < L ? p.scale * expf(e) : 0.f;
-    }
-    __syncwarp();
-    ok = ok && tc::mbar_wait(tc::smem_u32(&bars[i % kStages]), (i / kStages) & 1);
-    ++waited;
-    if (L < kC) {   // uniform: the tail rows are another sequence's
-      zero_tail_rows(kt, p.dk / 64, tid, L);
-      zero_tail_rows(kt + kTile, NV / 64, tid, L);
-      tc::fence_proxy_async_smem();
-      __syncthreads();
-    }
-    if (live || p.dk == 128) {
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {   // 32 tokens each
+          for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<uint4*>(kt + (quad >> 1) * kBlk + tc::sw128(r, (quad & 1) * 64 + 16 * b)) = make_uint4(0, 0, 0, 0);
+        }
+        __syncwarp();
+        zero_tail_rows(kt + kTile, NV / 64, tid, L);
+        tc::fence_proxy_async_smem();
+      }
+      const float decay_i = sh.decay[i & 1];
+      if (work) {
+        const float* ws = sh.w[i & 1] + 32 * part;
         uint32_t t1[16], t2[16], t3[16];
 #pragma unroll
         for (int q = 0; q < 16; ++q) {
-          const int r = 64 * half + 32 * b + 2 * q;   // (r & 7) is known at compile time: half and b move whole groups
-          const unsigned char* g8 = kt + (r >> 3) * 1024;
-          const float k0 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(g8 + off[(2 * q) & 7]) << 16);
-          const float k1 = __uint_as_float((uint32_t)*reinterpret_cast<const uint16_t*>(g8 + off[(2 * q + 1) & 7]) << 16);
-          const float2 wv = *reinterpret_cast<const float2*>(ws + 32 * b + 2 * q);
-          const float x0 = k0 * wv.x, x1 = k1 * wv.y;
-          t1[q] = pack_bf16(x0, x1);
-          const float2 f1 = unpack_bf16(t1[q]);
-          const float y0 = x0 - f1.x, y1 = x1 - f1.y;
-          t2[q] = pack_bf16(y0, y1);
-          const float2 f2 = unpack_bf16(t2[q]);
-          t3[q] = pack_bf16(y0 - f2.x, y1 - f2.y);
+          const unsigned char* g8 = kt + (q >> 2) * 1024;
+          const uint32_t k0 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * q) & 7]);
+          const uint32_t k1 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * q + 1) & 7]);
+          const float2 wv = *reinterpret_cast<const float2*>(ws + 2 * q);
+          const float2 x = __fmul2_rn(make_float2(__uint_as_float(k0 << 16), __uint_as_float(k1 << 16)), wv);
+          t1[q] = pack_bf16(x.x, x.y);
+          const float2 y = __ffma2_rn(unpack_bf16(t1[q]), neg, x);
+          t2[q] = pack_bf16(y.x, y.y);
+          const float2 z = __ffma2_rn(unpack_bf16(t2[q]), neg, y);
+          t3[q] = pack_bf16(z.x, z.y);
         }
-        const uint32_t at = TM_A + (i & 1) * 192 + 32 * half + 16 * b;
+        const uint32_t at = TM_A + (i & 1) * 192 + 16 * part;
         tmem_st16u(tc::tmem_addr(tmem, lane0, at), t1);
         tmem_st16u(tc::tmem_addr(tmem, lane0, at + 64), t2);
         tmem_st16u(tc::tmem_addr(tmem, lane0, at + 128), t3);
+        tc::tmem_st_wait();
       }
-      tc::tmem_st_wait();
-    }
-    tc::tc_fence_before();
-    if (i > 0) take(i - 1);
-    decay = expf((tt[0] + tt[1]) + (tt[2] + tt[3]));
-    log_decay += (tt[0] + tt[1]) + (tt[2] + tt[3]);
-    if (p.states && live) {   // the state before this chunk
-      const int64_t item = (slot0 + c) * Hv + h;
-      const int64_t term = (int64_t)p.dk * p.dv;
-      __nv_bfloat16* dst = p.states + item * p.terms * term +
-                           ((int64_t)((vt * NV + half * HC) / 64) * p.dk + row) * 64 + (half * HC) % 64;
+      if (i > 0) take(i - 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.aready));
+      decay = decay_i;
+      if (p.states && work) {   // the state before this chunk
+        const int64_t item = (int64_t)(slot0 + c) * Hv + h;
+        const int64_t term = (int64_t)p.dk * p.dv;
+        __nv_bfloat16* dst = p.states + item * p.terms * term +
+                             ((int64_t)((vt * NV + part * HC) / 64) * p.dk + row) * 64 + (vt * NV + part * HC) % 64;
 #pragma unroll
-      for (int j = 0; j < HC; j += 8) {
-        uint4 hi, lo;
-        split8(s + j, hi, lo);
-        const int64_t at = (int64_t)(j / 64) * p.dk * 64 + j % 64;
-        *reinterpret_cast<uint4*>(dst + at) = hi;
-        if (p.terms == 2) *reinterpret_cast<uint4*>(dst + term + at) = lo;
-      }
-    }
-    if (__syncthreads_or(!ok)) {
-      ok = false;
-      break;
-    }
-    if (tid == 0) {
-      tc::tc_fence_after();
-      const uint64_t bd = tc::make_sdesc(sbase + (i % kStages) * stage_bytes<NV>() + kTile, kBlk, 1024);
-#pragma unroll
-      for (int t = 0; t < 3; ++t)
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ta(tmem + TM_ACC, tmem + TM_A + (i & 1) * 192 + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc,
-                      t + ks > 0);
-      tc::mma_commit(bar_m);
-      if (i + 2 < steps) {   // its stage held step i - 1, whose product is complete
-        load(i + 2);
-        ++loaded;
+        for (int j = 0; j < HC; j += 8) {
+          uint4 hi, lo;
+          split8(s + j, hi, lo);
+          *reinterpret_cast<uint4*>(dst + j) = hi;
+          if (p.terms == 2) *reinterpret_cast<uint4*>(dst + term + j) = lo;
+        }
       }
     }
-    mma_issued = i + 1;
+    if (ok && steps) take(steps - 1);
   }
-  if (ok && steps) take(steps - 1);
-  if (tid == 0) {
-    // nothing of this CTA is in flight when it ends
-    for (int i = waited; i < loaded; ++i) tc::mbar_wait(tc::smem_u32(&bars[i % kStages]), (i / kStages) & 1, 1u << 22);
-    if (!ok && mma_issued) tc::mbar_wait(bar_m, (mma_issued - 1) & 1, 1u << 22);
+  if (!ok) {
+    *(volatile int*)&sh.dead = 1;
+    atomicExch(p.status, 1);
   }
+  __syncwarp();
   tc::tc_fence_before();
-  const bool all_ok = !__syncthreads_or(!ok);
+  __syncthreads();
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
-  if (!all_ok && tid == 0) atomicExch(p.status, 1);
-  if (!all_ok || !live) return;
+  if (sh.dead) return;
+  if (warp == kWorkers / 32) {
+    if (p.totals && lane == 0 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(log_decay);
+    return;
+  }
   float* dst = p.totals ? p.seg_tot + seg_g : p.sT && seg == p.nseg - 1 ? p.sT + sbase_g : nullptr;
-  if (dst)
+  if (dst && live)
 #pragma unroll
     for (int j = 0; j < HC; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
-  if (p.totals && tid == 0 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(log_decay);
 }
 
 // Segment contributions -> the state that each segment starts from (in place), element by element.
