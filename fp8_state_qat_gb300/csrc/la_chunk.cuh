@@ -26,17 +26,27 @@ struct Seqs {
 // (a NaN stays one)
 __device__ __forceinline__ float gate(float g) { return g < -110.f ? -110.f : g; }
 
-// Prefix sums of a chunk's log-decays within its four 32-token blocks, by one warp: lane l holds
-// token 32 j + l. Each is a pair hi + lo, so that a difference of two of them keeps its accuracy when a
-// large |g| (a reset) lies before both; decays across blocks are products of exponentials of
-// sums <= 0 of such differences, so nothing overflows and nothing cancels.
+// Prefix sums of a chunk's log-decays within its four 32-token blocks, by one warp: lane l holds the
+// four tokens 4 l + q, so a block is eight lanes. Each sum is a pair hi + lo, so that a difference of two
+// of them keeps its accuracy when a large |g| (a reset) lies before both; decays across blocks are
+// products of exponentials of sums <= 0 of such differences, so nothing overflows and nothing cancels.
 struct Gates {
   float hi[4], lo[4];   // inclusive prefix of the block
-  float thi[4], tlo[4]; // the block's total
+  float thi[4], tlo[4]; // the total of block j
+  float bhi, blo;       // of this lane's block
   __device__ __forceinline__ float tot(int j) const { return thi[j] + tlo[j]; }
-  // sum over the tokens after this lane's token of block j, up to the block's end
-  __device__ __forceinline__ float after(int j) const { return (thi[j] - hi[j]) + (tlo[j] - lo[j]); }
-  __device__ __forceinline__ float pre(int j) const { return hi[j] + lo[j]; }
+  // sum over the tokens after token q, up to its block's end
+  __device__ __forceinline__ float after(int q) const { return (bhi - hi[q]) + (blo - lo[q]); }
+  __device__ __forceinline__ float pre(int q) const { return hi[q] + lo[q]; }
+  // sums over the blocks before / after this lane's
+  __device__ __forceinline__ float blocks_before(int lane) const {
+    const int j = lane >> 3;
+    return j > 1 ? (j > 2 ? (tot(0) + tot(1)) + tot(2) : tot(0) + tot(1)) : (j ? tot(0) : 0.f);
+  }
+  __device__ __forceinline__ float blocks_after(int lane) const {
+    const int j = lane >> 3;
+    return j < 2 ? (j < 1 ? (tot(1) + tot(2)) + tot(3) : tot(2) + tot(3)) : (j < 3 ? tot(3) : 0.f);
+  }
 };
 
 struct GateSrc {
@@ -44,41 +54,80 @@ struct GateSrc {
   int Hv, head_decay;
   __device__ __forceinline__ void load(float (&x)[4], int64_t tok, int h, int L, int lane) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = 32 * j + lane;
-      x[j] = t < L ? gate(head_decay ? g[h] : g[(tok + t) * Hv + h]) : 0.f;
+    for (int q = 0; q < 4; ++q) {
+      const int t = 4 * lane + q;
+      x[q] = t < L ? gate(head_decay ? g[h] : g[(tok + t) * Hv + h]) : 0.f;
     }
   }
 };
 
+// (s, e) + (ys, ye) with s = fl(s + ys) and the rounding error carried in e
+__device__ __forceinline__ void add_pair(float& s, float& e, float ys, float ye) {
+  const float t = __fadd_rn(s, ys), b = __fsub_rn(t, s);
+  e += ye + __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(ys, b));
+  s = t;
+}
+
 __device__ __forceinline__ void scan_gates(const float (&x)[4], Gates& w, int lane) {
+  w.hi[0] = x[0];
+  w.lo[0] = 0.f;
+#pragma unroll
+  for (int q = 1; q < 4; ++q) {
+    w.hi[q] = x[q];
+    w.lo[q] = 0.f;
+    add_pair(w.hi[q], w.lo[q], w.hi[q - 1], w.lo[q - 1]);
+  }
+  float s = w.hi[3], e = w.lo[3];   // of the lanes before, within the block
+#pragma unroll
+  for (int off = 1; off < 8; off <<= 1) {
+    const float ys = __shfl_up_sync(0xffffffffu, s, off, 8), ye = __shfl_up_sync(0xffffffffu, e, off, 8);
+    if ((lane & 7) >= off) add_pair(s, e, ys, ye);
+  }
+  const float ps = __shfl_up_sync(0xffffffffu, s, 1, 8), pe = __shfl_up_sync(0xffffffffu, e, 1, 8);
+  if (lane & 7) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) add_pair(w.hi[q], w.lo[q], ps, pe);
+  }
+  // the block's total as its last token's prefix, so that nothing is left after that token
+  w.bhi = __shfl_sync(0xffffffffu, w.hi[3], lane | 7);
+  w.blo = __shfl_sync(0xffffffffu, w.lo[3], lane | 7);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    float s = x[j], e = 0.f;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const float ys = __shfl_up_sync(0xffffffffu, s, off), ye = __shfl_up_sync(0xffffffffu, e, off);
-      if (lane >= off) {
-        const float t = __fadd_rn(s, ys), b = __fsub_rn(t, s);     // two-sum: t + err = s + ys exactly
-        e += ye + __fadd_rn(__fsub_rn(s, __fsub_rn(t, b)), __fsub_rn(ys, b));
-        s = t;
-      }
-    }
-    w.hi[j] = s;
-    w.lo[j] = e;
-    w.thi[j] = __shfl_sync(0xffffffffu, s, 31);
-    w.tlo[j] = __shfl_sync(0xffffffffu, e, 31);
+    w.thi[j] = __shfl_sync(0xffffffffu, w.bhi, 8 * j);
+    w.tlo[j] = __shfl_sync(0xffffffffu, w.blo, 8 * j);
   }
 }
 
-// tcgen05 product with A in tensor memory (lane = row of A, each 32-bit column two bf16 of K)
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// tcgen05 products issued by the one lane of a converged warp whose `me` is set: the whole warp walks the
+// issuing code, so that its descriptors stay in uniform registers (inside a one-lane branch every product
+// moved them there anew and took about 130 cycles to issue).
+__device__ __forceinline__ void mma_bf16_w(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                           uint32_t accumulate, uint32_t me) {
   asm volatile(
-      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(
-          d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(me)
       : "memory");
+}
+// with A in tensor memory (lane = row of A, each 32-bit column two bf16 of K)
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate, uint32_t me) {
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0; "
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(me)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit_w(uint32_t mbar, uint32_t me) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %1, 0; "
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(mbar), "r"(me)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t me;
+  asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(me));
+  return me;
 }
 __device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* r) {
   asm volatile(

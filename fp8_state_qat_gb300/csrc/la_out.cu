@@ -65,7 +65,7 @@ struct __align__(16) Entry {
   float st[kC];                // decay between the state and the token, times f_st
   float hi[kC], lo[kC];        // prefix sums, for the pairwise decays
 };
-static_assert(offsetof(Entry, off) % 16 == 0 && offsetof(Entry, dcol) % 16 == 0, "read as float4");
+static_assert(offsetof(Entry, off) % 16 == 0 && offsetof(Entry, tot) % 16 == 0, "moved as float4");
 constexpr int kEntries = 2;
 constexpr uint32_t kSmemBytes = kRing * kTile + kEntries * sizeof(Entry) + 1024;
 static_assert(kSmemBytes <= 226 * 1024, "shared memory");
@@ -104,11 +104,11 @@ struct Shared {
   int dead;                          // a wait gave up: every role winds down
 };
 
-// Four K = 16 steps of a product from shared memory, by one lane.
+// Four K = 16 steps of a product from shared memory.
 __device__ __forceinline__ void mma4(uint32_t d, uint64_t a, uint32_t astep, uint64_t b, uint32_t bstep, uint32_t idesc,
-                                     bool first) {
+                                     bool first, uint32_t me) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) tc::mma_bf16(d, dadv(a, s * astep), dadv(b, s * bstep), idesc, !first || s > 0);
+  for (int s = 0; s < 4; ++s) mma_bf16_w(d, dadv(a, s * astep), dadv(b, s * bstep), idesc, !first || s > 0, me);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -219,40 +219,50 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
           e.h = it.h;
           e.role = it.role;
         }
-        int pairwise = 0;
-        float before = 0.f;   // log-decay from the state to the near edge of block j
+        // a block's own decays in two factors, both within exp(+-32), their product as exact as the prefix
+        // sums, while its range is at most 64; else pair by pair
+        float mx = g.pre(0), mn = mx;
 #pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          // the blocks in order of their distance from the state; j is known at compile time in both orders
-          float sum = 0.f;
-#pragma unroll
-          for (int m = 0; m < 4; ++m)
-            if (rev ? m > jj : m < jj) sum += g.tot(m);
-          before = sum;
-          const int t = 32 * jj + lane;
-          const float pre = g.pre(jj), aft = g.after(jj);
-          float mx = pre, mn = pre;
-#pragma unroll
-          for (int off = 16; off > 0; off >>= 1) {
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
-          }
-          // both factors stay within exp(+-32); their product is as exact as the prefix sums: while the
-          // range is 64, those of one float each
-          const float mid = 0.5f * (mx + mn);
-          if (!(mx - mn <= 64.f)) pairwise |= 1 << jj;
-          const float d = (g.hi[jj] - mid) + g.lo[jj];
-          const bool in = t < it.L;
-          e.off[t] = in ? expf(rev ? pre : aft) : 0.f;
-          e.drow[t] = expf(rev ? -d : d);
-          e.dcol[t] = expf(rev ? d : -d);
-          e.edge[t] = rev ? aft : pre;
-          e.st[t] = r.f_st * expf((rev ? aft : pre) + before);
-          e.hi[t] = g.hi[jj];
-          e.lo[t] = g.lo[jj];
-          if (lane == 0) e.tot[jj] = g.tot(jj);
+        for (int q = 1; q < 4; ++q) {
+          mx = fmaxf(mx, g.pre(q));
+          mn = fminf(mn, g.pre(q));
         }
-        if (lane == 0) e.pairwise = pairwise;
+#pragma unroll
+        for (int off = 4; off > 0; off >>= 1) {
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+          mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, off));
+        }
+        const float mid = 0.5f * (mx + mn);
+        const uint32_t wide = __ballot_sync(0xffffffffu, !(mx - mn <= 64.f));
+        const float near = rev ? g.blocks_after(lane) : g.blocks_before(lane);   // from the state to this block
+        float4 off4, dr, dcl, ed, st;
+        float* const po = &off4.x;
+        float* const pr = &dr.x;
+        float* const pc = &dcl.x;
+        float* const pe = &ed.x;
+        float* const ps = &st.x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float pre = g.pre(q), aft = g.after(q);
+          const float d = (g.hi[q] - mid) + g.lo[q];
+          const float up = expf(d), down = expf(-d);
+          po[q] = 4 * lane + q < it.L ? expf(rev ? pre : aft) : 0.f;
+          pr[q] = rev ? down : up;
+          pc[q] = rev ? up : down;
+          pe[q] = rev ? aft : pre;
+          ps[q] = r.f_st * expf((rev ? aft : pre) + near);
+        }
+        *reinterpret_cast<float4*>(e.off + 4 * lane) = off4;
+        *reinterpret_cast<float4*>(e.drow + 4 * lane) = dr;
+        *reinterpret_cast<float4*>(e.dcol + 4 * lane) = dcl;
+        *reinterpret_cast<float4*>(e.edge + 4 * lane) = ed;
+        *reinterpret_cast<float4*>(e.st + 4 * lane) = st;
+        *reinterpret_cast<float4*>(e.hi + 4 * lane) = make_float4(g.hi[0], g.hi[1], g.hi[2], g.hi[3]);
+        *reinterpret_cast<float4*>(e.lo + 4 * lane) = make_float4(g.lo[0], g.lo[1], g.lo[2], g.lo[3]);
+        if (lane == 0) {
+          *reinterpret_cast<float4*>(e.tot) = make_float4(g.tot(0), g.tot(1), g.tot(2), g.tot(3));
+          e.pairwise = (wide & 1) | (wide >> 8 & 1) << 1 | (wide >> 16 & 1) << 2 | (wide >> 24 & 1) << 3;
+        }
         i += gridDim.x;
         advance();
         if (i < items) p.gates.load(gx, it.tok, it.h, it.L, lane);
@@ -264,11 +274,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!more) break;
     }
   } else if (warp == 1) {
-    // ---- products: all lanes wait and compute descriptors, lane 0 issues ----
+    // ---- products: the warp stays converged, one lane issues ----
     uint32_t x = 0, k = 0;
+    const uint32_t me = elect_one();
     auto tile = [&](uint32_t y) { return sbase + (y % kRing) * kTile; };
     auto landed = [&](uint32_t y) { ok = ok && wait(sh.dead, sh.full[y % kRing], (y / kRing) & 1); };
-    auto release = [&](uint32_t y) { tc::mma_commit(tc::smem_u32(&sh.empty[y % kRing])); };
+    auto release = [&](uint32_t y) { mma_commit_w(tc::smem_u32(&sh.empty[y % kRing]), me); };
     auto good = [&] { return ok = __all_sync(0xffffffffu, ok); };
     while (true) {
       const uint32_t gs = k % kEntries;
@@ -289,7 +300,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         constexpr uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 128, false, false);
 #pragma unroll 1
         for (int b = 0; b < blocks; ++b)
-          if (lane == 0) mma4(tmem + d, dadv(ad, b * kBlk), 32, dadv(bd, b * kBlk), 32, idesc, b == 0);
+          mma4(tmem + d, dadv(ad, b * kBlk), 32, dadv(bd, b * kBlk), 32, idesc, b == 0, me);
       };
       landed(xb);
       landed(xa);
@@ -297,14 +308,14 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!good()) break;
       tc::tc_fence_after();
       scores(TM_S, tile(xa), tile(xb), na);
-      if (lane == 0) release(xb);
+      release(xb);
       if (dg) {
         landed(xc);
         landed(xe);
         if (!good()) break;
         scores(TM_E, tile(xe), tile(xc), nc);
       }
-      if (lane == 0) tc::mma_commit(tc::smem_u32(&sh.sc));
+      mma_commit_w(tc::smem_u32(&sh.sc), me);
       landed(xs);
       if (dg) landed(xs + 1);
       if (k > 0) ok = ok && wait(sh.dead, sh.ofree, (k - 1) & 1);
@@ -323,37 +334,33 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         const uint64_t bd = tc::make_sdesc(tile(xs + t), lbo, 1024);
 #pragma unroll 1
         for (int b = 0; b < na; ++b)
-          if (lane == 0) mma4(tmem + TM_I, dadv(ad, b * kBlk), 32, dadv(bd, b * kblk), kstep, idesc_s, t + b == 0);
+          mma4(tmem + TM_I, dadv(ad, b * kBlk), 32, dadv(bd, b * kblk), kstep, idesc_s, t + b == 0, me);
       }
-      if (lane == 0) {
-        release(xa);
-        release(xs);
-        if (dg) release(xs + 1);
-        tc::mma_commit(tc::smem_u32(&sh.oi));
-      }
-      __syncwarp();
+      release(xa);
+      release(xs);
+      if (dg) release(xs + 1);
+      mma_commit_w(tc::smem_u32(&sh.oi), me);
       landed(xc);
       ok = ok && wait(sh.dead, sh.pr, k & 1);
       if (!good()) break;
       tc::tc_fence_after();
-      if (lane == 0) {
+      {
         const uint64_t bd = tc::make_sdesc(tile(xc), kBlk, 1024);
         const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 64 * nc, false, true);
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks, dadv(bd, ks * 2048), idesc, ks > 0);
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks, dadv(bd, ks * 2048), idesc, ks > 0, me);
         release(xc);
-        tc::mma_commit(tc::smem_u32(&sh.oo));
+        mma_commit_w(tc::smem_u32(&sh.oo), me);
       }
-      __syncwarp();
       x += dg ? 6 : 4;
       ++k;
     }
     // the products in flight end before the tensor memory goes
     if (!ok) {
-      if (lane == 0) {
-        tc::mma_commit(tc::smem_u32(&sh.drain));
-        tc::mbar_wait(tc::smem_u32(&sh.drain), 0, 1u << 22);
-      }
+      __syncwarp();
+      mma_commit_w(tc::smem_u32(&sh.drain), me);
+      tc::mbar_wait(tc::smem_u32(&sh.drain), 0, 1u << 22);
     } else if (k > 0) {
       ok = wait(sh.dead, sh.oo, (k - 1) & 1);
     }

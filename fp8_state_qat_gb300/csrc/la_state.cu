@@ -26,7 +26,7 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 32;
+constexpr int kWorkers = 512, kThreads = kWorkers + 64;
 constexpr int kStages = 3;
 constexpr uint32_t TM_A = 0, TM_ACC = 384;   // two buffers of three 64-column A terms; the accumulator
 constexpr uint32_t kTmemCols = 512;
@@ -52,15 +52,16 @@ constexpr uint32_t smem_bytes() { return kStages * stage_bytes<NV>() + 1024; }
 struct Shared {
   uint64_t full[kStages];   // a step's tiles have landed
   uint64_t wready[2];       // its weights are written
+  uint64_t wfree[2];        // and read
   uint64_t aready;          // its A terms are written and the accumulator of the step before is read
   uint64_t mma;             // its product is complete
   uint32_t tmem;
   int dead;
-  float decay[2];
-  float w[2][kC];
+  float decay[2], pad[2];
+  float w[2][kC];           // read and written 16 bytes at a time
 };
 
-// Warps 0-15 weight K and hold the state; warp 16 loads, computes the weights and issues the products.
+// Warps 0-15 weight K and hold the state; warp 16 loads and issues the products; warp 17 computes the weights.
 template <int NV>
 __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty, const Params p) {
@@ -95,7 +96,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
 
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) tc::mbar_init(tc::smem_u32(&sh.full[i]), 1);
-    for (int i = 0; i < 2; ++i) tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
+      tc::mbar_init(tc::smem_u32(&sh.wfree[i]), kWorkers / 32);
+    }
     tc::mbar_init(tc::smem_u32(&sh.aready), kWorkers / 32);
     tc::mbar_init(tc::smem_u32(&sh.mma), 1);
     tc::mbar_fence_init();
@@ -111,7 +115,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   float s[HC];   // state elements (row, vt NV + part HC + j)
   const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * NV + part * HC;
   const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * NV + part * HC;
-  float log_decay = 0.f;   // of the whole segment (warp 16)
+  float log_decay = 0.f;   // of the whole segment (warp 17)
 
   if (warp == kWorkers / 32) {
     const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, NV, false, true);
@@ -123,52 +127,25 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, tok);
       for (int b = 0; b < NV / 64; ++b) tc::tma_load_3d(dst + kTile + b * kBlk, &ty, bar, vt * NV + 64 * b, h, tok);
     };
-    if (lane == 0)
-      for (; loaded < min(2, steps); ++loaded) load(loaded);
-    float gx[4];
-    auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
-    auto weights = [&](int i) {   // of step i, from gx
-      const int L = rows_of(chunk_of(i));
-      Gates w;
-      scan_gates(gx, w, lane);
-      if (i + 1 < steps) gates(i + 1);
-      const float tt[4] = {w.tot(0), w.tot(1), w.tot(2), w.tot(3)};
-      const float all = (tt[0] + tt[1]) + (tt[2] + tt[3]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float e = p.reverse ? w.pre(q) : w.after(q);
-#pragma unroll
-        for (int m = 0; m < 4; ++m)
-          if (p.reverse ? m < q : m > q) e += tt[m];
-        sh.w[i & 1][32 * q + lane] = 32 * q + lane < L ? p.scale * expf(e) : 0.f;
-      }
-      if (lane == 0) sh.decay[i & 1] = expf(all);
-      log_decay += all;
-      tc::mbar_arrive(tc::smem_u32(&sh.wready[i & 1]));
-    };
-    if (steps) {
-      gates(0);
-      weights(0);
-    }
+    for (; loaded < min(2, steps); ++loaded)
+      if (lane == 0) load(loaded);
+    const uint32_t me = elect_one();
     int issued = 0;
     for (int i = 0; i < steps; ++i) {
-      if (i + 1 < steps) weights(i + 1);   // the workers are past step i - 1, whose weights lie there
       ok = wait(sh.dead, sh.aready, i & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
-      if (lane == 0) {
-        const uint64_t bd = tc::make_sdesc(sbase + (i % kStages) * stage_bytes<NV>() + kTile, kBlk, 1024);
-        const uint32_t a = tmem + TM_A + (i & 1) * 192;
+      const uint64_t bd = tc::make_sdesc(sbase + (i % kStages) * stage_bytes<NV>() + kTile, kBlk, 1024);
+      const uint32_t a = tmem + TM_A + (i & 1) * 192;
 #pragma unroll
-        for (int t = 0; t < 3; ++t)
+      for (int t = 0; t < 3; ++t)
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_bf16_ta(tmem + TM_ACC, a + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc, t + ks > 0);
-        tc::mma_commit(tc::smem_u32(&sh.mma));
-        if (i + 2 < steps) {   // its stage held step i - 1, whose product the workers have taken
-          load(i + 2);
-          ++loaded;
-        }
+        for (int ks = 0; ks < 8; ++ks)
+          mma_bf16_ta(tmem + TM_ACC, a + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc, t + ks > 0, me);
+      mma_commit_w(tc::smem_u32(&sh.mma), me);
+      if (i + 2 < steps) {   // its stage held step i - 1, whose product the workers have taken
+        if (lane == 0) load(i + 2);
+        ++loaded;
       }
       __syncwarp();
       issued = i + 1;
@@ -177,6 +154,28 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       for (int i = max(0, loaded - kStages); i < loaded; ++i)
         tc::mbar_wait(tc::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, 1u << 22);
       if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma), (issued - 1) & 1, 1u << 22);
+    }
+  } else if (warp == kWorkers / 32 + 1) {
+    float gx[4];
+    auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
+    if (steps) gates(0);
+    for (int i = 0; i < steps; ++i) {
+      ok = wait(sh.dead, sh.wfree[i & 1], ((i >> 1) & 1) ^ 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      const int L = rows_of(chunk_of(i));
+      Gates w;
+      scan_gates(gx, w, lane);
+      if (i + 1 < steps) gates(i + 1);
+      const float all = (w.tot(0) + w.tot(1)) + (w.tot(2) + w.tot(3));
+      const float far = p.reverse ? w.blocks_before(lane) : w.blocks_after(lane);
+      float v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        v[q] = 4 * lane + q < L ? p.scale * expf((p.reverse ? w.pre(q) : w.after(q)) + far) : 0.f;
+      *reinterpret_cast<float4*>(&sh.w[i & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+      if (lane == 0) sh.decay[i & 1] = expf(all);
+      log_decay += all;
+      tc::mbar_arrive(tc::smem_u32(&sh.wready[i & 1]));
     }
   } else {
     const float* src = p.totals ? nullptr : p.nseg > 1 ? p.seg_tot + seg_g : p.s0 ? p.s0 + sbase_g : nullptr;
@@ -230,17 +229,22 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         const float* ws = sh.w[i & 1] + 32 * part;
         uint32_t t1[16], t2[16], t3[16];
 #pragma unroll
-        for (int q = 0; q < 16; ++q) {
+        for (int q = 0; q < 16; q += 2) {
           const unsigned char* g8 = kt + (q >> 2) * 1024;
-          const uint32_t k0 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * q) & 7]);
-          const uint32_t k1 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * q + 1) & 7]);
-          const float2 wv = *reinterpret_cast<const float2*>(ws + 2 * q);
-          const float2 x = __fmul2_rn(make_float2(__uint_as_float(k0 << 16), __uint_as_float(k1 << 16)), wv);
-          t1[q] = pack_bf16(x.x, x.y);
-          const float2 y = __ffma2_rn(unpack_bf16(t1[q]), neg, x);
-          t2[q] = pack_bf16(y.x, y.y);
-          const float2 z = __ffma2_rn(unpack_bf16(t2[q]), neg, y);
-          t3[q] = pack_bf16(z.x, z.y);
+          const float4 wv = *reinterpret_cast<const float4*>(ws + 2 * q);
+          const float2 w2[2] = {make_float2(wv.x, wv.y), make_float2(wv.z, wv.w)};
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int o = q + e;
+            const uint32_t k0 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * o) & 7]);
+            const uint32_t k1 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * o + 1) & 7]);
+            const float2 x = __fmul2_rn(make_float2(__uint_as_float(k0 << 16), __uint_as_float(k1 << 16)), w2[e]);
+            t1[o] = pack_bf16(x.x, x.y);
+            const float2 y = __ffma2_rn(unpack_bf16(t1[o]), neg, x);
+            t2[o] = pack_bf16(y.x, y.y);
+            const float2 z = __ffma2_rn(unpack_bf16(t2[o]), neg, y);
+            t3[o] = pack_bf16(z.x, z.y);
+          }
         }
         const uint32_t at = TM_A + (i & 1) * 192 + 16 * part;
         tmem_st16u(tc::tmem_addr(tmem, lane0, at), t1);
@@ -252,7 +256,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_before();
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.aready));
+      if (lane == 0) {
+        tc::mbar_arrive(tc::smem_u32(&sh.wfree[i & 1]));
+        tc::mbar_arrive(tc::smem_u32(&sh.aready));
+      }
       decay = decay_i;
       if (p.states && work) {   // the state before this chunk
         const int64_t item = (int64_t)(slot0 + c) * Hv + h;
@@ -280,8 +287,8 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
   if (sh.dead) return;
-  if (warp == kWorkers / 32) {
-    if (p.totals && lane == 0 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(log_decay);
+  if (warp >= kWorkers / 32) {
+    if (warp > kWorkers / 32 && p.totals && lane == 0 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(log_decay);
     return;
   }
   float* dst = p.totals ? p.seg_tot + seg_g : p.sT && seg == p.nseg - 1 ? p.sT + sbase_g : nullptr;
