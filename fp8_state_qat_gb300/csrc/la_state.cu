@@ -26,7 +26,7 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 64;
+constexpr int kWorkers = 512, kThreads = kWorkers + 96;
 constexpr int kStages = 3;
 constexpr uint32_t TM_A = 0, TM_ACC = 384;   // two buffers of three 64-column A terms; the accumulator
 constexpr uint32_t kTmemCols = 512;
@@ -57,11 +57,13 @@ struct Shared {
   uint64_t mma;             // its product is complete
   uint32_t tmem;
   int dead;
-  float decay[2], pad[2];
+  float decay[2], log_decay[2];   // Gam of a step; log Gam of the whole segment, in two parts
   float w[2][kC];           // read and written 16 bytes at a time
 };
 
-// Warps 0-15 weight K and hold the state; warp 16 loads and issues the products; warp 17 computes the weights.
+// Warps 0-15 weight K and hold the state; warp 16 loads and issues the products; warps 17
+// and 18 compute the weights, of every other step each: the latency of a step's loads and sums is longer than
+// the step.
 template <int NV>
 __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty, const Params p) {
@@ -115,7 +117,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   float s[HC];   // state elements (row, vt NV + part HC + j)
   const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * NV + part * HC;
   const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * NV + part * HC;
-  float log_decay = 0.f;   // of the whole segment (warp 17)
+  float log_decay = 0.f;   // of this warp's steps (warps 17, 18)
 
   if (warp == kWorkers / 32) {
     const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, NV, false, true);
@@ -155,17 +157,18 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         tc::mbar_wait(tc::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, 1u << 22);
       if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma), (issued - 1) & 1, 1u << 22);
     }
-  } else if (warp == kWorkers / 32 + 1) {
+  } else if (warp > kWorkers / 32) {
+    const int which = warp - kWorkers / 32 - 1;
     float gx[4];
     auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
-    if (steps) gates(0);
-    for (int i = 0; i < steps; ++i) {
+    if (which < steps) gates(which);
+    for (int i = which; i < steps; i += 2) {
       ok = wait(sh.dead, sh.wfree[i & 1], ((i >> 1) & 1) ^ 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const int L = rows_of(chunk_of(i));
       Gates w;
       scan_gates(gx, w, lane);
-      if (i + 1 < steps) gates(i + 1);
+      if (i + 2 < steps) gates(i + 2);
       const float all = (w.tot(0) + w.tot(1)) + (w.tot(2) + w.tot(3));
       const float far = p.reverse ? w.blocks_before(lane) : w.blocks_after(lane);
       float v[4];
@@ -177,6 +180,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       log_decay += all;
       tc::mbar_arrive(tc::smem_u32(&sh.wready[i & 1]));
     }
+    if (lane == 0) sh.log_decay[which] = log_decay;
   } else {
     const float* src = p.totals ? nullptr : p.nseg > 1 ? p.seg_tot + seg_g : p.s0 ? p.s0 + sbase_g : nullptr;
 #pragma unroll
@@ -208,6 +212,9 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       }
     };
     const float2 neg = make_float2(-1.f, -1.f);
+    const int64_t term = (int64_t)p.dk * p.dv, step = (int64_t)Hv * p.terms * term;   // a stored term; a chunk
+    __nv_bfloat16* dst = p.states + ((int64_t)(slot0 + (steps ? chunk_of(0) : 0)) * Hv + h) * p.terms * term +
+                         ((int64_t)((vt * NV + part * HC) / 64) * p.dk + row) * 64 + (vt * NV + part * HC) % 64;
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const int c = chunk_of(i), L = rows_of(c);
@@ -261,18 +268,20 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         tc::mbar_arrive(tc::smem_u32(&sh.aready));
       }
       decay = decay_i;
-      if (p.states && work) {   // the state before this chunk
-        const int64_t item = (int64_t)(slot0 + c) * Hv + h;
-        const int64_t term = (int64_t)p.dk * p.dv;
-        __nv_bfloat16* dst = p.states + item * p.terms * term +
-                             ((int64_t)((vt * NV + part * HC) / 64) * p.dk + row) * 64 + (vt * NV + part * HC) % 64;
+      if (p.states && live) {   // the state before this chunk
+        if (p.terms == 2) {
 #pragma unroll
-        for (int j = 0; j < HC; j += 8) {
-          uint4 hi, lo;
-          split8(s + j, hi, lo);
-          *reinterpret_cast<uint4*>(dst + j) = hi;
-          if (p.terms == 2) *reinterpret_cast<uint4*>(dst + term + j) = lo;
+          for (int j = 0; j < HC; j += 8) {
+            uint4 hi, lo;
+            split8(s + j, hi, lo);
+            *reinterpret_cast<uint4*>(dst + j) = hi;
+            *reinterpret_cast<uint4*>(dst + term + j) = lo;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < HC; j += 8) *reinterpret_cast<uint4*>(dst + j) = pack8(s + j);
         }
+        dst += p.reverse ? -step : step;
       }
     }
     if (ok && steps) take(steps - 1);
@@ -288,7 +297,8 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
   if (sh.dead) return;
   if (warp >= kWorkers / 32) {
-    if (warp > kWorkers / 32 && p.totals && lane == 0 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(log_decay);
+    if (p.totals && tid == kWorkers && vt == 0)
+      p.seg_dec[unit * p.nseg + seg] = expf(sh.log_decay[0] + sh.log_decay[1]);
     return;
   }
   float* dst = p.totals ? p.seg_tot + seg_g : p.sT && seg == p.nseg - 1 ? p.sT + sbase_g : nullptr;
