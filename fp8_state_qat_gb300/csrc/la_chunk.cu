@@ -24,9 +24,9 @@ struct DgParams {
   Seqs seqs;
   GateSrc gates;
   const float *rq, *rk, *aq, *bk;        // per (token, head): r, c, a, b
-  const __nv_bfloat16 *S, *dS;           // two terms each
+  const float* edge;                     // exp(gam_C) <S, dS> per item, in parts
+  int parts;
   float* dg;                             // [tokens, Hv], or per item with head_decay
-  int64_t elems;                         // dk dv
 };
 
 // One CTA of 128 threads per (chunk slot, head): thread = token.
@@ -48,29 +48,8 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
   }
   const int L = (int)(len - c * kC < kC ? len - c * kC : kC);
   __shared__ float red[3][4];
-  float gx[4];
-  Gates g;
-  p.gates.load(gx, tok, h, L, lane);
-  scan_gates(gx, g, lane);
-  const float decay = expf((g.tot(0) + g.tot(1)) + (g.tot(2) + g.tot(3)));
-  // <S, dS>, where the decay across the chunk leaves anything of it
-  float x = 0.f;
-  if (decay > 0.f) {
-    const uint4* s = reinterpret_cast<const uint4*>(p.S + item * 2 * p.elems);
-    const uint4* d = reinterpret_cast<const uint4*>(p.dS + item * 2 * p.elems);
-    const int n8 = (int)(p.elems / 8);
-#pragma unroll 2
-    for (int i = t; i < n8; i += kC) {
-      const uint4 q[4] = {s[i], s[i + n8], d[i], d[i + n8]};
-      const uint32_t* w = reinterpret_cast<const uint32_t*>(q);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 a = unpack_bf16(w[e]), al = unpack_bf16(w[4 + e]), b = unpack_bf16(w[8 + e]), bl = unpack_bf16(w[12 + e]);
-        x = fmaf(a.x + al.x, b.x + bl.x, x);
-        x = fmaf(a.y + al.y, b.y + bl.y, x);
-      }
-    }
-  }
+  // exp(gam_C) <S, dS>, from its parts (at most 32)
+  float x = t < p.parts ? p.edge[item * p.parts + t] : 0.f;
   const int64_t at = (tok + t) * Hv + h;
   float f = 0.f, b = 0.f;
   if (t < L) {
@@ -84,10 +63,10 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
     if (lane + off < 32) fs += yf;
     if (lane >= off) bs += yb;
   }
-  x = warp_sum(x);
+  if (warp == 0) x = warp_sum(x);
   if (lane == 0) {
     red[0][warp] = fs;
-    red[2][warp] = x;
+    if (warp == 0) red[2][0] = x;
   }
   if (lane == 31) red[1][warp] = bs;
   __syncthreads();
@@ -97,7 +76,7 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
     if (w > warp) after += red[0][w];
     if (w < warp) before += red[1][w];
   }
-  v = (v + (after + before)) + decay * ((red[2][0] + red[2][1]) + (red[2][2] + red[2][3]));
+  v = (v + (after + before)) + red[2][0];
   if (!p.gates.head_decay) {
     if (t < L) p.dg[at] = v;
     return;
@@ -142,7 +121,7 @@ __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, cons
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t S, dS, tot, dec, rq, rk, aq, bk, pq, pk, item, total;
+  size_t S, dS, tot, dec, rq, rk, aq, bk, edge, pq, pk, item, total;
 };
 Layout layout_of(const LaProblem& p, bool bwd) {
   const size_t items = (size_t)la_slots(p) * p.Hv, elems = (size_t)p.dk * p.dv, th = (size_t)p.B * p.T * p.Hv;
@@ -165,6 +144,7 @@ Layout layout_of(const LaProblem& p, bool bwd) {
     l.rk = take(th * 4);
     l.aq = take(th * 4);
     l.bk = take(th * 4);
+    l.edge = take(items * edge_parts(p) * 4);
     if (p.Hv != p.Hqk) {
       l.pq = take(th * p.dk * 4);
       l.pk = take(th * p.dk * 4);
@@ -189,11 +169,13 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
   int* const status = static_cast<int*>(ws);
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
-  StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec)};
+  StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
+             nullptr, nullptr};
   // o reads h0 through the states alone, so hT may be h0
   if ((e = launch_states(p, s, status, stream)) != cudaSuccess) return e;
-  OutRun o{p.q, p.k, p.v, nullptr, {base + l.S, nullptr}, {1, 1}, {}, 1};
-  o.role[0] = {0, 1, 2, -1, 0, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
+  // tiles k, q, v | S
+  OutRun o{{p.q, p.k, p.v, nullptr}, {base + l.S, nullptr}, {1, 1}, 3, {1, 0, 2, 0}, 1, {0}, {0}, {}, 1};
+  o.role[0] = {1, 0, 2, -1, 0, 1, 0x17, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
   return launch_outputs(p, o, status, stream);
 }
 
@@ -205,22 +187,24 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   const int G = p.Hv / p.Hqk;
   float *tot = (float*)(base + l.tot), *dec = (float*)(base + l.dec);
   float *rq = (float*)(base + l.rq), *rk = (float*)(base + l.rk), *aq = (float*)(base + l.aq), *bk = (float*)(base + l.bk);
+  float* const edge = (float*)(base + l.edge);
   float *pq = (float*)(base + l.pq), *pk = (float*)(base + l.pk);
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
-  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec};
+  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr};
   if ((e = launch_states(p, f, status, stream)) != cudaSuccess) return e;
-  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec};
+  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec, base + l.S, edge};
   if ((e = launch_states(p, b, status, stream)) != cudaSuccess) return e;
   if (tokens == 0 || items == 0)
     return p.head_decay ? cudaMemsetAsync(gr.dg, 0, (size_t)p.Hv * 4, stream) : cudaSuccess;
-  OutRun o{p.q, p.k, p.v, gr.dout, {base + l.S, base + l.dS}, {2, 2}, {}, 3};
-  o.role[0] = {3, 2, 1, 0, 0, 1, 0, p.scale, p.scale, G > 1 ? (void*)pq : gr.dq, G > 1, rq, aq};
-  o.role[1] = {2, 3, 0, 1, 1, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
-  o.role[2] = {1, 0, 3, -1, 1, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
+  // tiles v, q, k, do | S hi, lo, dS hi, lo
+  OutRun o{{p.q, p.k, p.v, gr.dout}, {base + l.S, base + l.dS}, {2, 2}, 4, {2, 0, 1, 3}, 4, {0, 0, 1, 1}, {0, 1, 0, 1}, {}, 3};
+  o.role[0] = {3, 0, 2, 1, 0, 2, 0x30, 1, 0, p.scale, p.scale, G > 1 ? (void*)pq : gr.dq, G > 1, rq, aq};
+  o.role[1] = {0, 3, 1, 2, 2, 2, 0x21, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
+  o.role[2] = {2, 1, 3, -1, 2, 1, 0x17, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
   if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
-  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, (const __nv_bfloat16*)(base + l.S),
-             (const __nv_bfloat16*)(base + l.dS), p.head_decay ? (float*)(base + l.item) : gr.dg, (int64_t)p.dk * p.dv};
+  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, edge, edge_parts(p),
+             p.head_decay ? (float*)(base + l.item) : gr.dg};
   la_dg_kernel<<<(unsigned)items, kC, 0, stream>>>(d);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (p.head_decay) {

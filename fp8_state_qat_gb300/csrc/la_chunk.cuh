@@ -176,15 +176,20 @@ struct StateRun {
   float scale;          // weight of every token's contribution
   float* seg_tot;       // split walks: [N Hv][nseg][dk][dv]
   float* seg_dec;       // [N Hv][nseg]
+  const void* other;    // two-term states S of the chunks, or null: then exp(gam_C) <S, state before the chunk>
+  float* edge;          // per item goes here, in edge_parts() parts
 };
+int edge_parts(const LaProblem& p);
 int state_segments(const LaProblem& p);
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream);
 
 // One family of outputs: out_t = f_in sum_s decay(t, s) (a_t . b_s) c_s + f_st decay_t a_t^T St,
 // s <= t with the state before the chunk (reverse 0), or s >= t with the state after it (reverse 1).
+// The operands are tiles of the chunk, by their places in OutRun's lists.
 struct Role {
-  int a, b, c, e;        // which of the maps q, k, v, do (0-3); e: rows dotted with the outputs, or -1
-  int st;                // which states (0: S, 1: dS)
+  int a, b, c, e;        // token tiles; e: rows dotted with the outputs, or -1
+  int st, terms;         // first state tile and the terms of the state that are used
+  int done;              // tiles that no later role of the chunk reads: bits 0-2 a, b, c; bits 4, 5 the state terms
   int st_transposed;     // St = S^T: the product is over the value columns
   int reverse;
   float f_in, f_st;
@@ -194,12 +199,11 @@ struct Role {
   float* dot_st;         // with e: e_t . (the state part of out_t)
 };
 struct OutRun {
-  const void* q;
-  const void* k;
-  const void* v;
-  const void* dout;
-  const void* states[2];
+  const void* tensor[4]; // q, k, v, dout
+  const void* states[2]; // S, dS
   int terms[2];
+  int ntok, tok[4];      // token tiles of a chunk, in the order of their release: which tensor
+  int nst, st[4], term[4];   // state tiles: which states, which term
   Role role[3];
   int roles;
 };

@@ -33,7 +33,7 @@ namespace la {
 namespace {
 
 constexpr int kThreads = 384;            // warps 0 TMA, 1 products, 2 gates, 4-7 scores, 8-11 outputs
-constexpr int kRing = 6;
+constexpr int kTok = 4, kSt = 2;          // rings of token and state tiles, 32 KB each
 constexpr uint32_t TM_S = 0, TM_E = 128, TM_I = 256, TM_O = 384;   // scores (P in place), e c^T, state part, P c
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSMs = 152;
@@ -44,6 +44,7 @@ struct Params {
   Role role[3];
   int heads[4], width[4];   // of q, k, v, do
   int terms[2];
+  int ntok, tok[4], nst, st[4], term[4];
   int* status;
   int slots, roles, dk, dv;
 };
@@ -67,17 +68,15 @@ struct __align__(16) Entry {
 };
 static_assert(offsetof(Entry, off) % 16 == 0 && offsetof(Entry, tot) % 16 == 0, "moved as float4");
 constexpr int kEntries = 2;
-constexpr uint32_t kSmemBytes = kRing * kTile + kEntries * sizeof(Entry) + 1024;
+constexpr uint32_t kSmemBytes = (kTok + kSt) * kTile + kEntries * sizeof(Entry) + 1024;
 static_assert(kSmemBytes <= 226 * 1024, "shared memory");
 
 struct Item {
-  int h, L, tok, role, state;   // state: index among the states
+  int h, L, tok, state;   // state: index among the states
 };
 
 // The item's chunk, or false where no chunk uses its slot.
 __device__ __forceinline__ bool locate(const Params& p, int i, Item& it) {
-  it.role = i % p.roles;
-  i /= p.roles;
   it.state = i;
   const int slot = i / p.gates.Hv;
   it.h = i - slot * p.gates.Hv;
@@ -95,10 +94,9 @@ __device__ __forceinline__ bool locate(const Params& p, int i, Item& it) {
 }
 
 struct Shared {
-  uint64_t full[kRing], empty[kRing];
+  uint64_t tfull[kTok], tempty[kTok], sfull[kSt], sempty[kSt];
   uint64_t gfull[kEntries], gempty[kEntries];
   uint64_t sc, oi, oo, pr, ofree;   // scores done, state part done, P c done, P written, accumulators read
-  uint64_t eread;                    // e read by every output thread
   uint64_t drain;
   uint32_t tmem;
   int dead;                          // a wait gave up: every role winds down
@@ -118,14 +116,19 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* const sm = smem_raw + (sbase - raw);
-  Entry* const entries = reinterpret_cast<Entry*>(sm + kRing * kTile);
+  Entry* const entries = reinterpret_cast<Entry*>(sm + (kTok + kSt) * kTile);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int items = p.slots * p.gates.Hv * p.roles;
+  const int items = p.slots * p.gates.Hv;
+  const uint32_t sstate = sbase + kTok * kTile;
 
   if (tid == 0) {
-    for (int i = 0; i < kRing; ++i) {
-      tc::mbar_init(tc::smem_u32(&sh.full[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh.empty[i]), 1);
+    for (int i = 0; i < kTok; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.tfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.tempty[i]), 1);
+    }
+    for (int i = 0; i < kSt; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.sfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.sempty[i]), 1);
     }
     for (int i = 0; i < kEntries; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.gfull[i]), 32);
@@ -137,7 +140,6 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     tc::mbar_init(tc::smem_u32(&sh.drain), 1);
     tc::mbar_init(tc::smem_u32(&sh.pr), 128);
     tc::mbar_init(tc::smem_u32(&sh.ofree), 128);
-    tc::mbar_init(tc::smem_u32(&sh.eread), 128);
     tc::mbar_fence_init();
     sh.dead = 0;
   }
@@ -148,53 +150,44 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
   const uint32_t tmem = sh.tmem;
   bool ok = true;
 
-  // Tiles of an item, in ring order: b, a, state, c -- with e: b, a, c, e, state hi, state lo.
-  if (tid == 0) {
-    uint32_t x = 0, slot = 0, turn = 0;   // tiles issued, x % kRing, (x / kRing) & 1
-    auto take_slot = [&](uint32_t bytes) {
-      if (!ok) return false;
-      ok = wait(sh.dead, sh.empty[slot], turn ^ 1);
-      if (ok) tc::mbar_expect_tx(tc::smem_u32(&sh.full[slot]), bytes);
-      return ok;
-    };
-    auto next = [&] {
-      ++x;
-      if (++slot == kRing) {
-        slot = 0;
-        turn ^= 1;
-      }
-    };
+  if (tid == 0 || tid == 96) {
+    // ---- loads: thread 0 the token tiles, thread 96 the state tiles, each as its slot falls free ----
+    const bool toks = tid == 0;
+    const int ring = toks ? kTok : kSt, per = toks ? p.ntok : p.nst;
+    uint64_t* const full = toks ? sh.tfull : sh.sfull;
+    uint64_t* const empty = toks ? sh.tempty : sh.sempty;
+    const uint32_t base = toks ? sbase : sstate;
+    int x = 0, slot = 0, turn = 0;   // tiles issued, x % ring, (x / ring) & 1
     for (int i = blockIdx.x; i < items && ok; i += gridDim.x) {
       Item it;
       if (!locate(p, i, it)) continue;
-      const Role& r = p.role[it.role];
-      const int n = r.e >= 0 ? 6 : 4;
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        // which tensor (0-3) or state term (4, 5) is tile j
-        const int m = j == 0 ? r.b : j == 1 ? r.a : n == 6 ? (j == 2 ? r.c : j == 3 ? r.e : j) : (j == 2 ? 4 : r.c);
-        if (m < 4) {
-          const int D = p.width[m], hh = it.h / (p.gates.Hv / p.heads[m]);
-          if (!take_slot(D / 64 * kBlk)) break;
-          const uint32_t dst = sbase + slot * kTile, bar = tc::smem_u32(&sh.full[slot]);
+      for (int j = 0; j < per; ++j) {
+        if (!(ok = wait(sh.dead, empty[slot], turn ^ 1))) break;
+        const uint32_t dst = base + slot * kTile, bar = tc::smem_u32(&full[slot]);
+        if (toks) {
+          const int m = p.tok[j], D = p.width[m], hh = it.h / (p.gates.Hv / p.heads[m]);
+          tc::mbar_expect_tx(bar, D / 64 * kBlk);
           for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &maps.t[m], bar, 64 * b, hh, it.tok);
         } else {
-          if (!take_slot(p.dk * p.dv * 2)) break;
-          const uint32_t dst = sbase + slot * kTile, bar = tc::smem_u32(&sh.full[slot]);
-          const int row = (it.state * p.terms[r.st] + (m - 4)) * p.dk * (p.dv / 64);
-          for (int b = 0; b < p.dv / 64; ++b)
-            tc::tma_load_2d(dst + b * p.dk * 128, &maps.s[r.st], bar, 0, row + b * p.dk);
+          const int w = p.st[j], row = (it.state * p.terms[w] + p.term[j]) * p.dk * (p.dv / 64);
+          tc::mbar_expect_tx(bar, p.dk * p.dv * 2);
+          for (int b = 0; b < p.dv / 64; ++b) tc::tma_load_2d(dst + b * p.dk * 128, &maps.s[w], bar, 0, row + b * p.dk);
         }
-        next();
+        ++x;
+        if (++slot == ring) {
+          slot = 0;
+          turn ^= 1;
+        }
       }
     }
     // no copy may be in flight when the CTA ends
-    for (uint32_t y = x > kRing ? x - kRing : 0; y < x; ++y)
-      tc::mbar_wait(tc::smem_u32(&sh.full[y % kRing]), (y / kRing) & 1, 1u << 22);
+    for (int y = max(0, x - ring); y < x; ++y)
+      tc::mbar_wait(tc::smem_u32(&full[y % ring]), (y / ring) & 1, 1u << 22);
   } else if (warp == 2) {
     // ---- gates: prefix sums and decay factors, one item ahead of the warps that use them ----
     uint32_t k = 0;
-    int i = blockIdx.x;
+    int i = blockIdx.x, role = 0;
     Item it;
     auto advance = [&] {
       while (i < items && !locate(p, i, it)) i += gridDim.x;
@@ -209,7 +202,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       Entry& e = entries[s];
       if (more) {
-        const Role& r = p.role[it.role];
+        const Role& r = p.role[role];
         const bool rev = r.reverse;
         Gates g;
         scan_gates(gx, g, lane);
@@ -217,7 +210,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
           e.tok = it.tok;
           e.L = it.L;
           e.h = it.h;
-          e.role = it.role;
+          e.role = role;
         }
         // a block's own decays in two factors, both within exp(+-32), their product as exact as the prefix
         // sums, while its range is at most 64; else pair by pair
@@ -263,9 +256,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
           *reinterpret_cast<float4*>(e.tot) = make_float4(g.tot(0), g.tot(1), g.tot(2), g.tot(3));
           e.pairwise = (wide & 1) | (wide >> 8 & 1) << 1 | (wide >> 16 & 1) << 2 | (wide >> 24 & 1) << 3;
         }
-        i += gridDim.x;
-        advance();
-        if (i < items) p.gates.load(gx, it.tok, it.h, it.L, lane);
+        if (++role == p.roles) {
+          role = 0;
+          i += gridDim.x;
+          advance();
+          if (i < items) p.gates.load(gx, it.tok, it.h, it.L, lane);
+        }
       } else if (lane == 0) {
         e.L = 0;
       }
@@ -275,11 +271,14 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     }
   } else if (warp == 1) {
     // ---- products: the warp stays converged, one lane issues ----
-    uint32_t x = 0, k = 0;
+    uint32_t x = 0, y = 0, k = 0;   // tiles of the chunks before; roles done
     const uint32_t me = elect_one();
-    auto tile = [&](uint32_t y) { return sbase + (y % kRing) * kTile; };
-    auto landed = [&](uint32_t y) { ok = ok && wait(sh.dead, sh.full[y % kRing], (y / kRing) & 1); };
-    auto release = [&](uint32_t y) { mma_commit_w(tc::smem_u32(&sh.empty[y % kRing]), me); };
+    auto ttile = [&](int j) { return sbase + ((x + j) % kTok) * kTile; };
+    auto stile = [&](int j) { return sstate + ((y + j) % kSt) * kTile; };
+    auto tlanded = [&](int j) { ok = ok && wait(sh.dead, sh.tfull[(x + j) % kTok], ((x + j) / kTok) & 1); };
+    auto slanded = [&](int j) { ok = ok && wait(sh.dead, sh.sfull[(y + j) % kSt], ((y + j) / kSt) & 1); };
+    auto trelease = [&](int j) { mma_commit_w(tc::smem_u32(&sh.tempty[(x + j) % kTok]), me); };
+    auto srelease = [&](int j) { mma_commit_w(tc::smem_u32(&sh.sempty[(y + j) % kSt]), me); };
     auto good = [&] { return ok = __all_sync(0xffffffffu, ok); };
     while (true) {
       const uint32_t gs = k % kEntries;
@@ -292,8 +291,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!more) break;
       const Role& r = p.role[role];
       const bool dg = r.e >= 0;
-      const int na = p.width[r.a] / 64, nc = p.width[r.c] / 64;
-      const uint32_t xb = x, xa = x + 1, xc = dg ? x + 2 : x + 3, xe = x + 3, xs = dg ? x + 4 : x + 2;
+      const int na = p.width[p.tok[r.a]] / 64, nc = p.width[p.tok[r.c]] / 64;
       // [128 x D] [128 x D]^T, both K-major
       auto scores = [&](uint32_t d, uint32_t ta, uint32_t tb, int blocks) {
         const uint64_t ad = tc::make_sdesc(ta, 16, 1024), bd = tc::make_sdesc(tb, 16, 1024);
@@ -302,22 +300,22 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         for (int b = 0; b < blocks; ++b)
           mma4(tmem + d, dadv(ad, b * kBlk), 32, dadv(bd, b * kBlk), 32, idesc, b == 0, me);
       };
-      landed(xb);
-      landed(xa);
+      tlanded(r.b);
+      tlanded(r.a);
       if (k > 0) ok = ok && wait(sh.dead, sh.oo, (k - 1) & 1);   // P of the item before is consumed
       if (!good()) break;
       tc::tc_fence_after();
-      scores(TM_S, tile(xa), tile(xb), na);
-      release(xb);
+      scores(TM_S, ttile(r.a), ttile(r.b), na);
+      if (r.done & 2) trelease(r.b);
       if (dg) {
-        landed(xc);
-        landed(xe);
+        tlanded(r.c);
+        tlanded(r.e);
         if (!good()) break;
-        scores(TM_E, tile(xe), tile(xc), nc);
+        scores(TM_E, ttile(r.e), ttile(r.c), nc);
       }
       mma_commit_w(tc::smem_u32(&sh.sc), me);
-      landed(xs);
-      if (dg) landed(xs + 1);
+      slanded(r.st);
+      if (r.terms > 1) slanded(r.st + 1);
       if (k > 0) ok = ok && wait(sh.dead, sh.ofree, (k - 1) & 1);
       if (!good()) break;
       tc::tc_fence_after();
@@ -328,32 +326,36 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
                                                : tc::make_idesc(tc::kKindBF16, 128, p.dv, false, true);
       const uint32_t lbo = r.st_transposed ? 16 : sblk, kstep = r.st_transposed ? 32 : 2048;
       const uint32_t kblk = r.st_transposed ? sblk : 8192;
-      const uint64_t ad = tc::make_sdesc(tile(xa), 16, 1024);
+      const uint64_t ad = tc::make_sdesc(ttile(r.a), 16, 1024);
 #pragma unroll 1
-      for (int t = 0; t < (dg ? 2 : 1); ++t) {
-        const uint64_t bd = tc::make_sdesc(tile(xs + t), lbo, 1024);
+      for (int t = 0; t < r.terms; ++t) {
+        const uint64_t bd = tc::make_sdesc(stile(r.st + t), lbo, 1024);
 #pragma unroll 1
         for (int b = 0; b < na; ++b)
           mma4(tmem + TM_I, dadv(ad, b * kBlk), 32, dadv(bd, b * kblk), kstep, idesc_s, t + b == 0, me);
       }
-      release(xa);
-      release(xs);
-      if (dg) release(xs + 1);
+      // tiles read by the output warps too (e) are released a role later, after the wait on ofree above
+      if (r.done & 1) trelease(r.a);
+      if (r.done & 16) srelease(r.st);
+      if (r.done & 32) srelease(r.st + 1);
       mma_commit_w(tc::smem_u32(&sh.oi), me);
-      landed(xc);
+      tlanded(r.c);
       ok = ok && wait(sh.dead, sh.pr, k & 1);
       if (!good()) break;
       tc::tc_fence_after();
       {
-        const uint64_t bd = tc::make_sdesc(tile(xc), kBlk, 1024);
+        const uint64_t bd = tc::make_sdesc(ttile(r.c), kBlk, 1024);
         const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 64 * nc, false, true);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
           mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks, dadv(bd, ks * 2048), idesc, ks > 0, me);
-        release(xc);
+        if (r.done & 4) trelease(r.c);
         mma_commit_w(tc::smem_u32(&sh.oo), me);
       }
-      x += dg ? 6 : 4;
+      if (role == p.roles - 1) {
+        x += p.ntok;
+        y += p.nst;
+      }
       ++k;
     }
     // the products in flight end before the tensor memory goes
@@ -449,17 +451,18 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       tc::tmem_st_wait();
       const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
       if (L < kC) {   // rows past the end of c would meet zero weights: not with a NaN
-        const uint32_t xc = dg ? x + 2 : x + 3;
-        ok = wait(sh.dead, sh.full[xc % kRing], (xc / kRing) & 1);
+        const uint32_t xc = x + r.c;
+        ok = wait(sh.dead, sh.tfull[xc % kTok], (xc / kTok) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        zero_tail_rows(sm + (xc % kRing) * kTile, p.width[r.c] / 64, tid - 128, L);
+        zero_tail_rows(sm + (xc % kTok) * kTile, p.width[p.tok[r.c]] / 64, tid - 128, L);
         tc::fence_proxy_async_smem();
       }
       tc::tc_fence_before();
       tc::mbar_arrive(tc::smem_u32(&sh.pr));
+      const int role = e.role;
       tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
       if (dg && row < L) r.dot_in[at] = r.f_in * (sum.x + sum.y);
-      x += dg ? 6 : 4;
+      if (role == p.roles - 1) x += p.ntok;
       ++k;
     }
   } else if (warp >= 8) {
@@ -467,7 +470,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     const int w = warp - 8;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
-    uint32_t x = 0, k = 0, dgs = 0;
+    uint32_t x = 0, k = 0;
     while (true) {
       const uint32_t gs = k % kEntries;
       ok = wait(sh.dead, sh.gfull[gs], (k / kEntries) & 1);
@@ -475,9 +478,10 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       const Entry& e = entries[gs];
       const int L = e.L;
       if (L == 0) break;
-      const Role& r = p.role[e.role];
+      const int role = e.role;
+      const Role& r = p.role[role];
       const bool dg = r.e >= 0;
-      const int nb = p.width[r.c] / 32;
+      const int nb = p.width[p.tok[r.c]] / 32;
       const float fs = e.st[row], fi = r.f_in;
       const int64_t at = (int64_t)(e.tok + row) * p.gates.Hv + e.h;
       tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
@@ -485,10 +489,10 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       if (dg) {
-        const uint32_t xe = x + 3;
-        ok = wait(sh.dead, sh.full[xe % kRing], (xe / kRing) & 1);   // landed long ago; makes it visible here
+        const uint32_t xe = x + r.e;
+        ok = wait(sh.dead, sh.tfull[xe % kTok], (xe / kTok) & 1);   // landed long ago; makes it visible here
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        const unsigned char* et = sm + (xe % kRing) * kTile;
+        const unsigned char* et = sm + (xe % kTok) * kTile;
         float2 dot[2] = {};
 #pragma unroll 1
         for (int b = 0; b < nb; ++b) {
@@ -534,16 +538,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       }
       tc::tc_fence_before();
       tc::mbar_arrive(tc::smem_u32(&sh.ofree));
-      if (dg) {   // all four warps read e; its slot is free when the last has
-        tc::mbar_arrive(tc::smem_u32(&sh.eread));
-        if (w == 0) {
-          ok = wait(sh.dead, sh.eread, dgs & 1);
-          if (!(ok = __all_sync(0xffffffffu, ok))) break;
-          if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.empty[(x + 3) % kRing]));
-        }
-        ++dgs;
-      }
-      x += dg ? 6 : 4;
+      if (role == p.roles - 1) x += p.ntok;
       ++k;
     }
   }
@@ -561,20 +556,36 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
 }  // namespace
 
 cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cudaStream_t stream) {
-  const int64_t tokens = (int64_t)p.B * p.T, slots = la_slots(p), items = slots * p.Hv * r.roles;   // < 2^24
+  const int64_t tokens = (int64_t)p.B * p.T, slots = la_slots(p), items = slots * p.Hv;   // < 2^22
   if (tokens == 0 || items == 0) return cudaSuccess;
   Maps m;
-  const void* base[4] = {r.q, r.k, r.v, r.dout};
-  Params o{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, {}, {p.Hqk, p.Hqk, p.Hv, p.Hv}, {p.dk, p.dk, p.dv, p.dv},
-           {r.terms[0], r.terms[1]}, status, (int)slots, r.roles, p.dk, p.dv};
+  Params o{};
+  o.seqs = {p.cu, p.T, p.N};
+  o.gates = {p.g, p.Hv, p.head_decay};
+  const int heads[4] = {p.Hqk, p.Hqk, p.Hv, p.Hv}, width[4] = {p.dk, p.dk, p.dv, p.dv};
   for (int i = 0; i < r.roles; ++i) o.role[i] = r.role[i];
-  for (int i = 0; i < 4; ++i)
-    if (!make_bf16_map(&m.t[i], base[i] ? base[i] : r.q, o.width[i], o.heads[i], tokens, kC)) return cudaErrorNotSupported;
+  for (int i = 0; i < 4; ++i) {
+    o.heads[i] = heads[i];
+    o.width[i] = width[i];
+    o.tok[i] = r.tok[i];
+    o.st[i] = r.st[i];
+    o.term[i] = r.term[i];
+    if (!make_bf16_map(&m.t[i], r.tensor[i] ? r.tensor[i] : r.tensor[2], width[i], heads[i], tokens, kC))
+      return cudaErrorNotSupported;
+  }
   for (int i = 0; i < 2; ++i) {
     const int j = r.states[i] ? i : 0;
+    o.terms[i] = r.terms[i];
     if (!make_bf16_rows_map(&m.s[i], r.states[j], slots * p.Hv * r.terms[j] * p.dk * (p.dv / 64), p.dk))
       return cudaErrorNotSupported;
   }
+  o.ntok = r.ntok;
+  o.nst = r.nst;
+  o.status = status;
+  o.slots = (int)slots;
+  o.roles = r.roles;
+  o.dk = p.dk;
+  o.dv = p.dv;
   cudaError_t e = cudaFuncSetAttribute(la_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   if (e != cudaSuccess) return e;
   la_out_kernel<<<(unsigned)std::min<int64_t>(items, kSMs), kThreads, kSmemBytes, stream>>>(m, o);

@@ -38,6 +38,8 @@ struct Params {
   float* sT;
   __nv_bfloat16* states;
   float *seg_tot, *seg_dec;
+  const __nv_bfloat16* other;
+  float* edge;
   int* status;
   int Hqk, dk, dv, terms, reverse, nseg;
   int totals;       // this launch computes the segments' contributions
@@ -215,6 +217,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     const int64_t term = (int64_t)p.dk * p.dv, step = (int64_t)Hv * p.terms * term;   // a stored term; a chunk
     __nv_bfloat16* dst = p.states + ((int64_t)(slot0 + (steps ? chunk_of(0) : 0)) * Hv + h) * p.terms * term +
                          ((int64_t)((vt * NV + part * HC) / 64) * p.dk + row) * 64 + (vt * NV + part * HC) % 64;
+    const __nv_bfloat16* oth = p.other + (dst - p.states);   // the same place of the other states (both two terms)
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const int c = chunk_of(i), L = rows_of(c);
@@ -259,6 +262,13 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         tmem_st16u(tc::tmem_addr(tmem, lane0, at + 128), t3);
         tc::tmem_st_wait();
       }
+      if (p.other && live) {   // S of this chunk, needed once the state is known
+#pragma unroll
+        for (int j = 0; j < HC; j += 16) {
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(oth + j));
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(oth + term + j));
+        }
+      }
       if (i > 0) take(i - 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_before();
@@ -282,6 +292,24 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           for (int j = 0; j < HC; j += 8) *reinterpret_cast<uint4*>(dst + j) = pack8(s + j);
         }
         dst += p.reverse ? -step : step;
+      }
+      if (p.other) {
+        float2 x = make_float2(0.f, 0.f);
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < HC; j += 8) {
+            const uint4 h = *reinterpret_cast<const uint4*>(oth + j), l = *reinterpret_cast<const uint4*>(oth + term + j);
+            const uint32_t hu[4] = {h.x, h.y, h.z, h.w}, lu[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              x = __ffma2_rn(__fadd2_rn(unpack_bf16(hu[q]), unpack_bf16(lu[q])),
+                             make_float2(s[j + 2 * q], s[j + 2 * q + 1]), x);
+          }
+        }
+        const float sum = warp_sum(x.x + x.y);
+        if (lane == 0)
+          p.edge[(((int64_t)(slot0 + c) * Hv + h) * tiles + vt) * (kWorkers / 32) + warp] = decay_i * sum;
+        oth += p.reverse ? -step : step;
       }
     }
     if (ok && steps) take(steps - 1);
@@ -352,6 +380,12 @@ int state_segments(const LaProblem& p) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kSMs / walks, chunks / 4));
 }
 
+// A tile of 128 value columns weights K once for both halves, but has half as many CTAs.
+static bool wide_tiles(const LaProblem& p) {
+  return p.dv == 128 && (int64_t)p.N * p.Hv * state_segments(p) >= kSMs;
+}
+int edge_parts(const LaProblem& p) { return (wide_tiles(p) ? 1 : p.dv / 64) * (kWorkers / 32); }
+
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream) {
   const int64_t units = (int64_t)p.N * p.Hv, tokens = (int64_t)p.B * p.T;
   if (units == 0) return cudaSuccess;
@@ -365,13 +399,13 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cu
   if (!make_bf16_map(&tx, r.x, p.dk, p.Hqk, tokens, kC) || !make_bf16_map(&ty, r.y, p.dv, p.Hv, tokens, kC))
     return cudaErrorNotSupported;
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, (__nv_bfloat16*)r.states, r.seg_tot, r.seg_dec,
-           status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.scale};
-  // a tile of 128 value columns weights K once for both halves, but has half as many CTAs
-  const bool wide = p.dv == 128 && units * s.nseg >= kSMs;
+           (const __nv_bfloat16*)r.other, r.edge, status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.scale};
+  const bool wide = wide_tiles(p);
   auto go = [&] { return wide ? run<128>(tx, ty, s, units, stream) : run<64>(tx, ty, s, units, stream); };
   if (s.nseg > 1) {
     s.totals = 1;
     s.states = nullptr;
+    s.other = nullptr;
     cudaError_t e = go();
     if (e != cudaSuccess) return e;
     la_join_kernel<<<dim3((unsigned)((elems / 4 + 255) / 256), (unsigned)units), 256, 0, stream>>>(
@@ -379,6 +413,7 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cu
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     s.totals = 0;
     s.states = (__nv_bfloat16*)r.states;
+    s.other = (const __nv_bfloat16*)r.other;
   }
   return go();
 }
