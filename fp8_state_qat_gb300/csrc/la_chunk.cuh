@@ -1,6 +1,8 @@
 // la_chunk.cuh -- pieces shared by the chunked linear-attention kernels (128-token chunks).
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "la.h"
 #include "tc_common.cuh"
@@ -161,6 +163,19 @@ __device__ __forceinline__ bool wait(int& dead, uint64_t& bar, uint32_t parity) 
   const uint32_t a = tc::smem_u32(&bar);
   if (GDN_WAIT_LIMIT > 0 && tc::mbar_try_wait(a, parity)) return true;
   return wait_slow(&dead, a, parity);
+}
+
+// cudaFuncSetAttribute(MaxDynamicSharedMemorySize), once per kernel and device
+template <class K>
+inline cudaError_t allow_smem(K kernel, uint32_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 // ---- launchers of the parts (la_state.cu, la_out.cu) ----

@@ -570,13 +570,13 @@ cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cud
     o.tok[i] = r.tok[i];
     o.st[i] = r.st[i];
     o.term[i] = r.term[i];
-    if (!make_bf16_map(&m.t[i], r.tensor[i] ? r.tensor[i] : r.tensor[2], width[i], heads[i], tokens, kC))
-      return cudaErrorNotSupported;
+    if (!r.tensor[i]) m.t[i] = m.t[0];   // not used
+    else if (!make_bf16_map(&m.t[i], r.tensor[i], width[i], heads[i], tokens, kC)) return cudaErrorNotSupported;
   }
   for (int i = 0; i < 2; ++i) {
-    const int j = r.states[i] ? i : 0;
     o.terms[i] = r.terms[i];
-    if (!make_bf16_rows_map(&m.s[i], r.states[j], slots * p.Hv * r.terms[j] * p.dk * (p.dv / 64), p.dk))
+    if (!r.states[i]) m.s[i] = m.s[0];   // not used
+    else if (!make_bf16_rows_map(&m.s[i], r.states[i], slots * p.Hv * r.terms[i] * p.dk * (p.dv / 64), p.dk))
       return cudaErrorNotSupported;
   }
   o.ntok = r.ntok;
@@ -586,7 +586,8 @@ cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cud
   o.roles = r.roles;
   o.dk = p.dk;
   o.dv = p.dv;
-  cudaError_t e = cudaFuncSetAttribute(la_out_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(la_out_kernel, kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
   la_out_kernel<<<(unsigned)std::min<int64_t>(items, kSMs), kThreads, kSmemBytes, stream>>>(m, o);
   return cudaGetLastError();

@@ -355,8 +355,8 @@ constexpr int kSMs = 152;
 
 template <int NV>
 cudaError_t run(const CUtensorMap& tx, const CUtensorMap& ty, const Params& p, int64_t units, cudaStream_t stream) {
-  cudaError_t e = cudaFuncSetAttribute(la_state_kernel<NV>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       smem_bytes<NV>());
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(la_state_kernel<NV>, smem_bytes<NV>(), allowed);
   if (e != cudaSuccess) return e;
   la_state_kernel<NV><<<(unsigned)(units * p.nseg * (p.dv / NV)), kThreads, smem_bytes<NV>(), stream>>>(tx, ty, p);
   return cudaGetLastError();
