@@ -36,20 +36,23 @@ struct Params {
   GateSrc gates;
   const float* s0;
   float* sT;
-  __nv_bfloat16* states;
   float *seg_tot, *seg_dec;
-  const __nv_bfloat16* other;
   float* edge;
   int* status;
   int Hqk, dk, dv, terms, reverse, nseg;
   int totals;       // this launch computes the segments' contributions
+  int store, other; // the states are stored; <S, state> is computed
   float scale;
 };
 
 template <int NV>
 constexpr uint32_t stage_bytes() { return kTile + NV / 64 * kBlk; }
 template <int NV>
-constexpr uint32_t smem_bytes() { return kStages * stage_bytes<NV>() + 1024; }
+constexpr uint32_t off_stage() { return kStages * stage_bytes<NV>(); }   // states on their way out: 32 KB
+template <int NV>
+constexpr uint32_t off_other() { return off_stage<NV>() + kTile; }         // S of the chunk, hi and lo (NV 64)
+template <int NV>
+constexpr uint32_t smem_bytes() { return off_other<NV>() + (NV == 64 ? kTile : 0) + 1024; }
 
 struct Shared {
   uint64_t full[kStages];   // a step's tiles have landed
@@ -57,10 +60,12 @@ struct Shared {
   uint64_t wfree[2];        // and read
   uint64_t aready;          // its A terms are written and the accumulator of the step before is read
   uint64_t mma;             // its product is complete
+  uint64_t sfree;           // the states written out are read from shared memory
+  uint64_t ofull, oread;    // S of the step has landed; is read
   uint32_t tmem;
   int dead;
   float decay[2], log_decay[2];   // Gam of a step; log Gam of the whole segment, in two parts
-  float w[2][kC];           // read and written 16 bytes at a time
+  __align__(16) float w[2][kC];   // read and written 16 bytes at a time
 };
 
 // Warps 0-15 weight K and hold the state; warp 16 loads and issues the products; warps 17
@@ -68,7 +73,8 @@ struct Shared {
 // the step.
 template <int NV>
 __global__ void __launch_bounds__(kThreads, 1)
-la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty, const Params p) {
+la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
+                const __grid_constant__ CUtensorMap ts, const __grid_constant__ CUtensorMap to, const Params p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(16) Shared sh;
   constexpr int HC = NV / 4;   // value columns a thread
@@ -106,6 +112,9 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     }
     tc::mbar_init(tc::smem_u32(&sh.aready), kWorkers / 32);
     tc::mbar_init(tc::smem_u32(&sh.mma), 1);
+    tc::mbar_init(tc::smem_u32(&sh.sfree), 1);
+    tc::mbar_init(tc::smem_u32(&sh.ofull), 1);
+    tc::mbar_init(tc::smem_u32(&sh.oread), kWorkers / 32);
     tc::mbar_fence_init();
     sh.dead = 0;
   }
@@ -131,8 +140,22 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, tok);
       for (int b = 0; b < NV / 64; ++b) tc::tma_load_3d(dst + kTile + b * kBlk, &ty, bar, vt * NV + 64 * b, h, tok);
     };
+    auto state_row = [&](int i, int terms, int term) {   // of the stored states: this value tile's rows
+      const int item = (slot0 + chunk_of(i)) * Hv + h;
+      return ((item * terms + term) * (p.dv / 64) + vt * (NV / 64)) * p.dk;
+    };
+    auto load_other = [&](int i) {
+      tc::mbar_expect_tx(tc::smem_u32(&sh.ofull), 2 * p.dk * 128);
+      for (int t = 0; t < 2; ++t)
+        tc::tma_load_2d(sbase + off_other<NV>() + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
+    };
     for (; loaded < min(2, steps); ++loaded)
       if (lane == 0) load(loaded);
+    int others = 0;
+    if (p.other && steps) {
+      if (lane == 0) load_other(0);
+      others = 1;
+    }
     const uint32_t me = elect_one();
     int issued = 0;
     for (int i = 0; i < steps; ++i) {
@@ -147,17 +170,38 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         for (int ks = 0; ks < 8; ++ks)
           mma_bf16_ta(tmem + TM_ACC, a + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc, t + ks > 0, me);
       mma_commit_w(tc::smem_u32(&sh.mma), me);
+      issued = i + 1;
       if (i + 2 < steps) {   // its stage held step i - 1, whose product the workers have taken
         if (lane == 0) load(i + 2);
         ++loaded;
       }
+      if (p.store) {
+        if (lane == 0) {
+          for (int b = 0; b < (NV == 64 ? p.terms : 2); ++b)
+            tc::tma_store_2d(&ts, sbase + off_stage<NV>() + b * kBlk, 0,
+                             NV == 64 ? state_row(i, p.terms, b) : state_row(i, 1, 0) + b * p.dk);
+          tc::bulk_commit();
+        }
+        __syncwarp();
+      }
+      if (p.other && i + 1 < steps) {
+        ok = wait(sh.dead, sh.oread, i & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) load_other(i + 1);
+        ++others;
+      }
+      if (p.store && lane == 0) {
+        tc::bulk_wait_read();
+        tc::mbar_arrive(tc::smem_u32(&sh.sfree));
+      }
       __syncwarp();
-      issued = i + 1;
     }
     if (lane == 0 && !ok) {   // nothing of this CTA is in flight when it ends
       for (int i = max(0, loaded - kStages); i < loaded; ++i)
         tc::mbar_wait(tc::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, 1u << 22);
       if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma), (issued - 1) & 1, 1u << 22);
+      if (others) tc::mbar_wait(tc::smem_u32(&sh.ofull), (others - 1) & 1, 1u << 22);
+      tc::bulk_wait_read();
     }
   } else if (warp > kWorkers / 32) {
     const int which = warp - kWorkers / 32 - 1;
@@ -214,10 +258,6 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       }
     };
     const float2 neg = make_float2(-1.f, -1.f);
-    const int64_t term = (int64_t)p.dk * p.dv, step = (int64_t)Hv * p.terms * term;   // a stored term; a chunk
-    __nv_bfloat16* dst = p.states + ((int64_t)(slot0 + (steps ? chunk_of(0) : 0)) * Hv + h) * p.terms * term +
-                         ((int64_t)((vt * NV + part * HC) / 64) * p.dk + row) * 64 + (vt * NV + part * HC) % 64;
-    const __nv_bfloat16* oth = p.other + (dst - p.states);   // the same place of the other states (both two terms)
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const int c = chunk_of(i), L = rows_of(c);
@@ -262,15 +302,25 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         tmem_st16u(tc::tmem_addr(tmem, lane0, at + 128), t3);
         tc::tmem_st_wait();
       }
-      if (p.other && live) {   // S of this chunk, needed once the state is known
-#pragma unroll
-        for (int j = 0; j < HC; j += 16) {
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(oth + j));
-          asm volatile("prefetch.global.L1 [%0];" ::"l"(oth + term + j));
-        }
-      }
       if (i > 0) take(i - 1);
+      if (p.store && i > 0) ok = ok && wait(sh.dead, sh.sfree, (i - 1) & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (p.store && live) {   // the state before this chunk, 128-byte swizzled rows of 64 columns
+#pragma unroll
+        for (int j = 0; j < HC; j += 8) {
+          const int col = part * HC + j;
+          unsigned char* at = sm + off_stage<NV>() + (col / 64) * kBlk + tc::sw128(row, (col % 64) * 2);
+          if (NV == 64 && p.terms == 2) {
+            uint4 hi, lo;
+            split8(s + j, hi, lo);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + kBlk) = lo;
+          } else {
+            *reinterpret_cast<uint4*>(at) = pack8(s + j);
+          }
+        }
+        tc::fence_proxy_async_smem();
+      }
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
@@ -278,38 +328,27 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         tc::mbar_arrive(tc::smem_u32(&sh.aready));
       }
       decay = decay_i;
-      if (p.states && live) {   // the state before this chunk
-        if (p.terms == 2) {
-#pragma unroll
-          for (int j = 0; j < HC; j += 8) {
-            uint4 hi, lo;
-            split8(s + j, hi, lo);
-            *reinterpret_cast<uint4*>(dst + j) = hi;
-            *reinterpret_cast<uint4*>(dst + term + j) = lo;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < HC; j += 8) *reinterpret_cast<uint4*>(dst + j) = pack8(s + j);
-        }
-        dst += p.reverse ? -step : step;
-      }
-      if (p.other) {
+      if (NV == 64 && p.other) {
+        ok = wait(sh.dead, sh.ofull, i & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         float2 x = make_float2(0.f, 0.f);
         if (live) {
 #pragma unroll
           for (int j = 0; j < HC; j += 8) {
-            const uint4 h = *reinterpret_cast<const uint4*>(oth + j), l = *reinterpret_cast<const uint4*>(oth + term + j);
-            const uint32_t hu[4] = {h.x, h.y, h.z, h.w}, lu[4] = {l.x, l.y, l.z, l.w};
+            const unsigned char* at = sm + off_other<NV>() + tc::sw128(row, (part * HC + j) * 2);
+            const uint4 hv = *reinterpret_cast<const uint4*>(at), lv = *reinterpret_cast<const uint4*>(at + kBlk);
+            const uint32_t hu[4] = {hv.x, hv.y, hv.z, hv.w}, lu[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               x = __ffma2_rn(__fadd2_rn(unpack_bf16(hu[q]), unpack_bf16(lu[q])),
                              make_float2(s[j + 2 * q], s[j + 2 * q + 1]), x);
           }
         }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.oread));
         const float sum = warp_sum(x.x + x.y);
         if (lane == 0)
           p.edge[(((int64_t)(slot0 + c) * Hv + h) * tiles + vt) * (kWorkers / 32) + warp] = decay_i * sum;
-        oth += p.reverse ? -step : step;
       }
     }
     if (ok && steps) take(steps - 1);
@@ -354,11 +393,11 @@ __global__ void __launch_bounds__(256) la_join_kernel(float* seg_tot, const floa
 constexpr int kSMs = 152;
 
 template <int NV>
-cudaError_t run(const CUtensorMap& tx, const CUtensorMap& ty, const Params& p, int64_t units, cudaStream_t stream) {
+cudaError_t run(const CUtensorMap (&m)[4], const Params& p, int64_t units, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(la_state_kernel<NV>, smem_bytes<NV>(), allowed);
   if (e != cudaSuccess) return e;
-  la_state_kernel<NV><<<(unsigned)(units * p.nseg * (p.dv / NV)), kThreads, smem_bytes<NV>(), stream>>>(tx, ty, p);
+  la_state_kernel<NV><<<(unsigned)(units * p.nseg * (p.dv / NV)), kThreads, smem_bytes<NV>(), stream>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
 }
 
@@ -380,11 +419,12 @@ int state_segments(const LaProblem& p) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kSMs / walks, chunks / 4));
 }
 
-// A tile of 128 value columns weights K once for both halves, but has half as many CTAs.
+// A tile of 128 value columns weights K once for both halves, but has half as many CTAs and no room in
+// shared memory for second terms.
 static bool wide_tiles(const LaProblem& p) {
   return p.dv == 128 && (int64_t)p.N * p.Hv * state_segments(p) >= kSMs;
 }
-int edge_parts(const LaProblem& p) { return (wide_tiles(p) ? 1 : p.dv / 64) * (kWorkers / 32); }
+int edge_parts(const LaProblem& p) { return p.dv / 64 * (kWorkers / 32); }
 
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream) {
   const int64_t units = (int64_t)p.N * p.Hv, tokens = (int64_t)p.B * p.T;
@@ -395,25 +435,29 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cu
     return r.s0 ? cudaMemcpyAsync(r.sT, r.s0, units * elems * 4, cudaMemcpyDeviceToDevice, stream)
                 : cudaMemsetAsync(r.sT, 0, units * elems * 4, stream);
   }
-  CUtensorMap tx, ty;
-  if (!make_bf16_map(&tx, r.x, p.dk, p.Hqk, tokens, kC) || !make_bf16_map(&ty, r.y, p.dv, p.Hv, tokens, kC))
+  CUtensorMap m[4];
+  if (!make_bf16_map(&m[0], r.x, p.dk, p.Hqk, tokens, kC) || !make_bf16_map(&m[1], r.y, p.dv, p.Hv, tokens, kC))
     return cudaErrorNotSupported;
-  Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, (__nv_bfloat16*)r.states, r.seg_tot, r.seg_dec,
-           (const __nv_bfloat16*)r.other, r.edge, status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.scale};
-  const bool wide = wide_tiles(p);
-  auto go = [&] { return wide ? run<128>(tx, ty, s, units, stream) : run<64>(tx, ty, s, units, stream); };
+  m[2] = m[3] = m[0];   // where not used
+  const int64_t rows = la_slots(p) * p.Hv * p.dk * (p.dv / 64);   // of one term
+  if (r.states && !make_bf16_rows_map(&m[2], r.states, rows * r.terms, p.dk)) return cudaErrorNotSupported;
+  if (r.other && !make_bf16_rows_map(&m[3], r.other, rows * 2, p.dk)) return cudaErrorNotSupported;
+  Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
+           status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
+           r.scale};
+  const bool wide = wide_tiles(p) && r.terms == 1;
+  auto go = [&] { return wide ? run<128>(m, s, units, stream) : run<64>(m, s, units, stream); };
   if (s.nseg > 1) {
     s.totals = 1;
-    s.states = nullptr;
-    s.other = nullptr;
+    s.store = s.other = 0;
     cudaError_t e = go();
     if (e != cudaSuccess) return e;
     la_join_kernel<<<dim3((unsigned)((elems / 4 + 255) / 256), (unsigned)units), 256, 0, stream>>>(
         r.seg_tot, r.seg_dec, r.s0, s.nseg, elems);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     s.totals = 0;
-    s.states = (__nv_bfloat16*)r.states;
-    s.other = (const __nv_bfloat16*)r.other;
+    s.store = r.states != nullptr;
+    s.other = r.other != nullptr;
   }
   return go();
 }
