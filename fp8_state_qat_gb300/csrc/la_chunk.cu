@@ -23,7 +23,8 @@ namespace {
 struct DgParams {
   Seqs seqs;
   GateSrc gates;
-  const float *rq, *rk, *aq, *bk;        // per (token, head): r, c, a, b
+  const float *rq, *rk, *aq, *bk;        // per (token, head): r and c in two parts, a, b
+  int64_t th;                            // tokens x heads
   const float* edge;                     // exp(gam_C) <S, dS> per item, in parts
   int parts;
   float* dg;                             // [tokens, Hv], or per item with head_decay
@@ -53,7 +54,7 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
   const int64_t at = (tok + t) * Hv + h;
   float f = 0.f, b = 0.f;
   if (t < L) {
-    f = (p.rq[at] - p.rk[at]) + p.aq[at];
+    f = ((p.rq[at] + p.rq[p.th + at]) - (p.rk[at] + p.rk[p.th + at])) + p.aq[at];
     b = p.bk[at];
   }
   float fs = f, bs = b;   // suffix sums of f, prefix sums of b, both with the own token
@@ -140,8 +141,8 @@ Layout layout_of(const LaProblem& p, bool bwd) {
     l.dec = take((size_t)p.N * p.Hv * nseg * 4);
   }
   if (bwd) {
-    l.rq = take(th * 4);
-    l.rk = take(th * 4);
+    l.rq = take(th * 8);
+    l.rk = take(th * 8);
     l.aq = take(th * 4);
     l.bk = take(th * 4);
     l.edge = take(items * edge_parts(p) * 4);
@@ -203,7 +204,7 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   o.role[1] = {0, 3, 1, 2, 2, 2, 0x21, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
   o.role[2] = {2, 1, 3, -1, 2, 1, 0x17, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
   if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
-  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, edge, edge_parts(p),
+  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, tokens * p.Hv, edge, edge_parts(p),
              p.head_decay ? (float*)(base + l.item) : gr.dg};
   la_dg_kernel<<<(unsigned)items, kC, 0, stream>>>(d);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;

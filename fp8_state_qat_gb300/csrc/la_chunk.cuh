@@ -210,7 +210,7 @@ struct Role {
   float f_in, f_st;
   void* out;             // bf16 [tokens, Hv, dc] (fp32 with out_f32)
   int out_f32;
-  float* dot_in;         // with e: sum_{s != t} decay (a_t . b_s) (e_t . c_s) f_in per (token, head)
+  float* dot_in;         // with e: sum_{s != t} decay (a_t . b_s) (e_t . c_s) f_in per (token, head), in two parts
   float* dot_st;         // with e: e_t . (the state part of out_t)
 };
 struct OutRun {

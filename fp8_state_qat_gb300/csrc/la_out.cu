@@ -32,7 +32,7 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kThreads = 384;            // warps 0 TMA, 1 products, 2 gates, 4-7 scores, 8-11 outputs
+constexpr int kThreads = 512;            // warps 0, 3 TMA, 1 products, 2 gates, 4-11 scores, 12-15 outputs
 constexpr int kTok = 4, kSt = 2;          // rings of token and state tiles, 32 KB each
 constexpr uint32_t TM_S = 0, TM_E = 128, TM_I = 256, TM_O = 384;   // scores (P in place), e c^T, state part, P c
 constexpr uint32_t kTmemCols = 512;
@@ -46,6 +46,7 @@ struct Params {
   int terms[2];
   int ntok, tok[4], nst, st[4], term[4];
   int* status;
+  int64_t dot_stride;       // between the two halves of dot_in
   int slots, roles, dk, dv;
 };
 struct Maps {
@@ -68,7 +69,8 @@ struct __align__(16) Entry {
 };
 static_assert(offsetof(Entry, off) % 16 == 0 && offsetof(Entry, tot) % 16 == 0, "moved as float4");
 constexpr int kEntries = 2;
-constexpr uint32_t kSmemBytes = (kTok + kSt) * kTile + kEntries * sizeof(Entry) + 1024;
+constexpr uint32_t kOffOut = (kTok + kSt) * kTile + kEntries * sizeof(Entry);   // 4 KB for each output warp
+constexpr uint32_t kSmemBytes = kOffOut + 4 * 4096 + 1024;
 static_assert(kSmemBytes <= 226 * 1024, "shared memory");
 
 struct Item {
@@ -132,13 +134,13 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     }
     for (int i = 0; i < kEntries; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.gfull[i]), 32);
-      tc::mbar_init(tc::smem_u32(&sh.gempty[i]), 1 + 128 + 128);
+      tc::mbar_init(tc::smem_u32(&sh.gempty[i]), 1 + 256 + 128);
     }
     tc::mbar_init(tc::smem_u32(&sh.sc), 1);
     tc::mbar_init(tc::smem_u32(&sh.oi), 1);
     tc::mbar_init(tc::smem_u32(&sh.oo), 1);
     tc::mbar_init(tc::smem_u32(&sh.drain), 1);
-    tc::mbar_init(tc::smem_u32(&sh.pr), 128);
+    tc::mbar_init(tc::smem_u32(&sh.pr), 256);
     tc::mbar_init(tc::smem_u32(&sh.ofree), 128);
     tc::mbar_fence_init();
     sh.dead = 0;
@@ -348,7 +350,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 64 * nc, false, true);
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks, dadv(bd, ks * 2048), idesc, ks > 0, me);
+          mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks + (ks & 4) * 8, dadv(bd, ks * 2048), idesc, ks > 0, me);
         if (r.done & 4) trelease(r.c);
         mma_commit_w(tc::smem_u32(&sh.oo), me);
       }
@@ -366,9 +368,9 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     } else if (k > 0) {
       ok = wait(sh.dead, sh.oo, (k - 1) & 1);
     }
-  } else if (warp >= 4 && warp < 8) {
-    // ---- scores -> weighted, masked, bf16 P; with e the pair sums of dg ----
-    const int w = warp - 4;
+  } else if (warp >= 4 && warp < 12) {
+    // ---- scores -> weighted, masked, bf16 P; with e the pair sums of dg. Two warps for 32 rows, 64 columns each ----
+    const int w = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
     uint32_t x = 0, k = 0;
@@ -388,12 +390,13 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       tc::tc_fence_after();
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 2 * half; j < 2 * half + 2; ++j) {
         uint32_t u[16];
+        const uint32_t pcol = TM_S + 64 * half + 16 * (j & 1);   // over scores that this warp alone reads, before
         if (rev ? j < w : j > w) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) u[c] = 0;
-          tmem_st16u(tc::tmem_addr(tmem, lane0, TM_S + 16 * j), u);
+          tmem_st16u(tc::tmem_addr(tmem, lane0, pcol), u);
           continue;
         }
         const bool diag = j == w;
@@ -434,8 +437,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         }
 #pragma unroll
         for (int c = 0; c < 16; ++c) u[c] = pack_bf16(v[2 * c], v[2 * c + 1]);
-        // columns [16 j, 16 j + 16) hold scores of blocks <= j / 2, read before
-        tmem_st16u(tc::tmem_addr(tmem, lane0, TM_S + 16 * j), u);
+        tmem_st16u(tc::tmem_addr(tmem, lane0, pcol), u);
         if (dg) {
           if (diag) mask &= ~(1u << lane);   // pairs of different tokens
           float ev[32];
@@ -454,20 +456,21 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         const uint32_t xc = x + r.c;
         ok = wait(sh.dead, sh.tfull[xc % kTok], (xc / kTok) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        zero_tail_rows(sm + (xc % kTok) * kTile, p.width[p.tok[r.c]] / 64, tid - 128, L);
+        if (half == 0) zero_tail_rows(sm + (xc % kTok) * kTile, p.width[p.tok[r.c]] / 64, tid - 128, L);
         tc::fence_proxy_async_smem();
       }
       tc::tc_fence_before();
       tc::mbar_arrive(tc::smem_u32(&sh.pr));
       const int role = e.role;
       tc::mbar_arrive(tc::smem_u32(&sh.gempty[gs]));
-      if (dg && row < L) r.dot_in[at] = r.f_in * (sum.x + sum.y);
+      if (dg && row < L) r.dot_in[half * p.dot_stride + at] = r.f_in * (sum.x + sum.y);
       if (role == p.roles - 1) x += p.ntok;
       ++k;
     }
-  } else if (warp >= 8) {
+  } else if (warp >= 12) {
     // ---- outputs ----
-    const int w = warp - 8;
+    const int w = warp - 12;
+    unsigned char* const stage = sm + kOffOut + 4096 * w;
     const uint32_t lane0 = 32u * w;
     const int row = 32 * w + lane;
     uint32_t x = 0, k = 0;
@@ -513,6 +516,23 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       const float2 fs2 = make_float2(fs, fs), fi2 = make_float2(fi, fi);
+      // 128-byte pieces of the 32 rows go through shared memory, so that a store instruction covers whole
+      // lines of 4 rows instead of 16 bytes in each of 32
+      const int esz = r.out_f32 ? 4 : 2;
+      const int64_t rstride = (int64_t)p.gates.Hv * 32 * nb * esz;
+      unsigned char* dst = static_cast<unsigned char*>(r.out) + (at - (int64_t)(lane - (lane >> 3)) * p.gates.Hv) * (32 * nb * esz) +
+                           (lane & 7) * 16;   // row 32 w + lane / 8, piece lane % 8
+      auto flush = [&] {
+        __syncwarp();
+#pragma unroll
+        for (int m = 0; m < 8; ++m) {
+          const int q = 4 * m + (lane >> 3);
+          const uint4 x16 = *reinterpret_cast<const uint4*>(stage + q * 128 + (((lane & 7) ^ (q & 7)) << 4));
+          if (32 * w + q < L) *reinterpret_cast<uint4*>(dst + 4 * m * rstride) = x16;
+        }
+        dst += 128;
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int b = 0; b < nb; ++b) {
         float v[32], s[32];
@@ -524,16 +544,17 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
           v[c] = o.x;
           v[c + 1] = o.y;
         }
-        if (row < L) {
-          if (r.out_f32) {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(r.out) + at * (32 * nb) + 32 * b);
+        if (r.out_f32) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) dst[c] = make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) + at * (32 * nb) + 32 * b);
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<float4*>(stage + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+                make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+          flush();
+        } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) dst[c] = pack8(v + 8 * c);
-          }
+          for (int c = 0; c < 4; ++c)
+            *reinterpret_cast<uint4*>(stage + lane * 128 + (((4 * (b & 1) + c) ^ (lane & 7)) << 4)) = pack8(v + 8 * c);
+          if (b & 1) flush();
         }
       }
       tc::tc_fence_before();
@@ -579,6 +600,7 @@ cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cud
     else if (!make_bf16_rows_map(&m.s[i], r.states[i], slots * p.Hv * r.terms[i] * p.dk * (p.dv / 64), p.dk))
       return cudaErrorNotSupported;
   }
+  o.dot_stride = tokens * p.Hv;
   o.ntok = r.ntok;
   o.nst = r.nst;
   o.status = status;
