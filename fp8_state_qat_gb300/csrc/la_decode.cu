@@ -17,10 +17,10 @@
 namespace gdn {
 namespace {
 
-// fl32(x / s): three fused multiply-adds with the rounded reciprocal r of s (see quotient() in
-// common.cuh) for a normal s, else the IEEE divide
-__device__ __forceinline__ float div_by_scale(float x, float s, float r) {
-  return s >= 1.0e-30f ? quotient(x, s, r) : __fdiv_rn(x, s);
+// fl32(x / s) for two elements: paired fused multiply-adds with the rounded reciprocal (quotient2() in
+// common.cuh) for a normal s, else the IEEE divide. `normal` is the same for a whole tile.
+__device__ __forceinline__ float2 div2(float2 x, float s, float2 ns2, float2 r2, bool normal) {
+  return normal ? quotient2(x, ns2, r2) : make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s));
 }
 
 __device__ __forceinline__ float scale_of(float amax, float inv_max) {
@@ -44,7 +44,7 @@ la_decode_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __res
   const int64_t base = unit * DK * dv + col;
   float4 s[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) s[i] = *reinterpret_cast<const float4*>(state + base + (int64_t)(rg + 8 * i) * dv);
+  for (int i = 0; i < R; ++i) s[i] = __ldcs(reinterpret_cast<const float4*>(state + base + (int64_t)(rg + 8 * i) * dv));
   const __nv_bfloat16* kp = k + ((int64_t)n * Hqk + hq) * DK;
   const __nv_bfloat16* qp = q + ((int64_t)n * Hqk + hq) * DK;
   const float a = expf(g[unit]);
@@ -86,10 +86,11 @@ la_decode_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __res
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const float sc = scale_of(fmaxf(m[i], rmax[warp ^ 1][rg + 8 * i]), 1.f / kInt8Max), rc = __frcp_rn(sc);
-      s[i].x = __fmul_rn(rintf(div_by_scale(s[i].x, sc, rc)), sc);
-      s[i].y = __fmul_rn(rintf(div_by_scale(s[i].y, sc, rc)), sc);
-      s[i].z = __fmul_rn(rintf(div_by_scale(s[i].z, sc, rc)), sc);
-      s[i].w = __fmul_rn(rintf(div_by_scale(s[i].w, sc, rc)), sc);
+      const float2 ns2 = make_float2(-sc, -sc), r2 = make_float2(rc, rc);
+      const float2 a = div2(make_float2(s[i].x, s[i].y), sc, ns2, r2, sc >= 1.0e-30f);
+      const float2 b = div2(make_float2(s[i].z, s[i].w), sc, ns2, r2, sc >= 1.0e-30f);
+      s[i] = make_float4(__fmul_rn(rintf(a.x), sc), __fmul_rn(rintf(a.y), sc), __fmul_rn(rintf(b.x), sc),
+                         __fmul_rn(rintf(b.y), sc));
     }
   } else if (state_qdq) {
     __shared__ float wmax[4];
@@ -97,17 +98,21 @@ la_decode_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __res
     if (lane == 0) wmax[warp] = amax;
     __syncthreads();
     const float sc = scale_of(fmaxf(fmaxf(wmax[0], wmax[1]), fmaxf(wmax[2], wmax[3])), 1.f / kE4M3Max);
-    const float rc = __frcp_rn(sc);
+    const float2 ns2 = make_float2(-sc, -sc), r2 = make_float2(__frcp_rn(sc), __frcp_rn(sc));
+    auto qdq = [&](bool normal) {
 #pragma unroll
-    for (int i = 0; i < R; ++i) {
-      const __nv_fp8x2_e4m3 c01(make_float2(div_by_scale(s[i].x, sc, rc), div_by_scale(s[i].y, sc, rc)));
-      const __nv_fp8x2_e4m3 c23(make_float2(div_by_scale(s[i].z, sc, rc), div_by_scale(s[i].w, sc, rc)));
-      const float2 f01 = static_cast<float2>(c01), f23 = static_cast<float2>(c23);
-      s[i] = make_float4(__fmul_rn(f01.x, sc), __fmul_rn(f01.y, sc), __fmul_rn(f23.x, sc), __fmul_rn(f23.y, sc));
-    }
+      for (int i = 0; i < R; ++i) {
+        const __nv_fp8x2_e4m3 c01(div2(make_float2(s[i].x, s[i].y), sc, ns2, r2, normal));
+        const __nv_fp8x2_e4m3 c23(div2(make_float2(s[i].z, s[i].w), sc, ns2, r2, normal));
+        const float2 f01 = static_cast<float2>(c01), f23 = static_cast<float2>(c23);
+        s[i] = make_float4(__fmul_rn(f01.x, sc), __fmul_rn(f01.y, sc), __fmul_rn(f23.x, sc), __fmul_rn(f23.y, sc));
+      }
+    };
+    if (sc >= 1.0e-30f) qdq(true);
+    else qdq(false);
   }
 #pragma unroll
-  for (int i = 0; i < R; ++i) *reinterpret_cast<float4*>(state_out + base + (int64_t)(rg + 8 * i) * dv) = s[i];
+  for (int i = 0; i < R; ++i) __stcs(reinterpret_cast<float4*>(state_out + base + (int64_t)(rg + 8 * i) * dv), s[i]);
 }
 
 }  // namespace

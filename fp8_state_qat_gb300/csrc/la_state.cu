@@ -43,6 +43,8 @@ struct Params {
   int totals;       // this launch computes the segments' contributions
   int store, other; // the states are stored; <S, state> is computed
   float scale;
+  int sorted;
+  uint8_t order[64];   // the sequences, longest first
 };
 
 template <int NV>
@@ -92,10 +94,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const int vt = u % tiles;
   u /= tiles;
   const int seg = u % p.nseg;
-  const int unit = u / p.nseg;
+  u /= p.nseg;
   if (p.totals && seg == p.nseg - 1) return;   // nothing follows the last segment
   const int Hv = p.gates.Hv;
-  const int n = unit / Hv, h = unit % Hv, hq = h / (Hv / p.Hqk);
+  const int n = p.sorted ? p.order[u / Hv] : u / Hv, h = u % Hv, unit = n * Hv + h, hq = h / (Hv / p.Hqk);
   const int t0 = (int)p.seqs.start(n), len = (int)p.seqs.len(n), slot0 = (int)p.seqs.slot0(n);
   const int nch = len / kC + (len % kC != 0);
   const int per = (nch + p.nseg - 1) / p.nseg;
@@ -445,6 +447,15 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cu
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
            status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
            r.scale};
+  // Walks of unequal lengths: the longest first, so that the last ones to start are short (b = 1, 8 packed
+  // sequences of 1 to 8192 tokens, 32 heads: 200 -> 177 us). Many sequences even out by themselves.
+  if (p.cu_host && p.N <= 64) {
+    s.sorted = 1;
+    for (int i = 0; i < p.N; ++i) s.order[i] = (uint8_t)i;
+    std::stable_sort(s.order, s.order + p.N, [&](uint8_t a, uint8_t b) {
+      return p.cu_host[a + 1] - p.cu_host[a] > p.cu_host[b + 1] - p.cu_host[b];
+    });
+  }
   const bool wide = wide_tiles(p) && r.terms == 1;
   auto go = [&] { return wide ? run<128>(m, s, units, stream) : run<64>(m, s, units, stream); };
   if (s.nseg > 1) {

@@ -27,12 +27,6 @@ namespace {
 
 constexpr int E = 8;                  // elements a thread
 
-__device__ __forceinline__ void load8f(const float* p, float* v) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8f(const __nv_bfloat16* p, float* v) { load_bf16x8(p, v); }
 __device__ __forceinline__ void store8f(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
@@ -48,19 +42,33 @@ __device__ __forceinline__ float tof(__nv_bfloat16 x) { return __bfloat162float(
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// The 8 elements of thread t of a row; columns past D read as zero and are not written.
+// The 8 elements of thread t of a row as they lie in memory, so that the next row's loads can be in flight
+// while a row is worked on; columns past D and rows past the end are zero.
+template <int TPR, bool VEC, class T>
+struct Raw {
+  __align__(16) T x[E];
+  __device__ __forceinline__ void load(const T* row, bool live, int D, int t) {
+    if (VEC) {
+      constexpr int N = E * sizeof(T) / 16;
+      uint4* r = reinterpret_cast<uint4*>(x);
+      const uint4* p = reinterpret_cast<const uint4*>(row + 8 * t);
+#pragma unroll
+      for (int i = 0; i < N; ++i) r[i] = live && 8 * t < D ? p[i] : make_uint4(0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = live && t + TPR * e < D ? row[t + TPR * e] : T(0.f);
+    }
+  }
+  __device__ __forceinline__ void get(float* v) const {
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = tof(x[e]);
+  }
+};
 template <int TPR, bool VEC, class T>
 __device__ __forceinline__ void load_row(const T* row, int D, int t, float* v) {
-  if (VEC) {
-    if (8 * t < D) load8f(row + 8 * t, v);
-    else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = t + TPR * e < D ? tof(row[t + TPR * e]) : 0.f;
-  }
+  Raw<TPR, VEC, T> r;
+  r.load(row, true, D, t);
+  r.get(v);
 }
 template <int TPR, bool VEC, class T>
 __device__ __forceinline__ void store_row(T* row, int D, int t, const float* v) {
@@ -80,6 +88,9 @@ __device__ __forceinline__ void load_w(const void* w, int w_bf16, int D, int t, 
 }
 
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Resident CTAs an SM that a backward's registers leave room for (and its launch asks for): its rows in flight
+// need about 100 registers a thread.
+constexpr int bwd_per_sm(int tpr) { return tpr <= 256 ? 2 : 1; }
 
 // Sums of M values over the TPR threads of a row, the same in each of them. `slot` alternates
 // between calls, so that one barrier a call is enough.
@@ -112,8 +123,9 @@ struct RowSum {
   }
 };
 
-// silu(z) = z / (1 + exp(-z)) and its derivative; exp(-z) = inf gives 0 as it should
-__device__ __forceinline__ float sigmoidf(float z) { return 1.f / (1.f + expf(-z)); }
+// 1 / (1 + exp(-z)) from the hardware's exponential and reciprocal: a few units in 2^-22 for |z| up to 10, far
+// below the rounding of what it goes into; exp(-z) = inf gives 0. The IEEE forms made the kernel issue-bound.
+__device__ __forceinline__ float sigmoidf(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
 
 template <int TPR, bool VEC, class X>
 __global__ void __launch_bounds__(threads_of(TPR))
@@ -126,19 +138,24 @@ gated_norm_fwd_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__
   float wv[E];
   load_w<TPR, VEC>(w, w_bf16, D, t, wv);
   const float inv_d = 1.f / (float)D;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
-    const int64_t r = r0 + rg;
+  Raw<TPR, VEC, X> nx;
+  Raw<TPR, VEC, __nv_bfloat16> nz;
+  const int64_t stride = (int64_t)gridDim.x * RPC;
+  int64_t r = (int64_t)blockIdx.x * RPC + rg;
+  nx.load(x + r * D, r < rows, D, t);
+  nz.load(z + r * D, r < rows, D, t);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += stride, r += stride) {
     const bool live = r < rows;
-    float xv[E] = {}, zv[E] = {};
-    if (live) {
-      load_row<TPR, VEC>(x + r * D, D, t, xv);
-      load_row<TPR, VEC>(z + r * D, D, t, zv);
-    }
+    float xv[E], zv[E];
+    nx.get(xv);
+    nz.get(zv);
+    nx.load(x + (r + stride) * D, r + stride < rows, D, t);
+    nz.load(z + (r + stride) * D, r + stride < rows, D, t);
     float s[1] = {0.f};
 #pragma unroll
     for (int e = 0; e < E; ++e) s[0] = fmaf(xv[e], xv[e], s[0]);
     RowSum<TPR, 1>::run(s, sm, slot);
-    const float rs = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float rs = rsqrtf(fmaf(s[0], inv_d, eps));
     if (live) {
       float o[E];
 #pragma unroll
@@ -173,7 +190,7 @@ __device__ __forceinline__ void write_partials(float (&acc)[M][E], float* red, f
 // With n = rms(x), s = silu(z), d = dy w s (the gradient at n):
 //   dx = r (d - n mean(d n)),  dz = dy n w silu'(z),  dw = sum over rows of dy n s
 template <int TPR, bool VEC, class X>
-__global__ void __launch_bounds__(threads_of(TPR))
+__global__ void __launch_bounds__(threads_of(TPR), bwd_per_sm(TPR))
 gated_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dy, const X* __restrict__ x,
                       const __nv_bfloat16* __restrict__ z, const void* __restrict__ w, int w_bf16,
                       X* __restrict__ dx, __nv_bfloat16* __restrict__ dz, float* __restrict__ part, int64_t rows,
@@ -186,15 +203,22 @@ gated_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dy, const X* __restrict_
   float wv[E], acc[1][E] = {};
   load_w<TPR, VEC>(w, w_bf16, D, t, wv);
   const float inv_d = 1.f / (float)D;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
-    const int64_t r = r0 + rg;
+  Raw<TPR, VEC, X> nx;
+  Raw<TPR, VEC, __nv_bfloat16> nz, nd;
+  const int64_t stride = (int64_t)gridDim.x * RPC;
+  int64_t r = (int64_t)blockIdx.x * RPC + rg;
+  nx.load(x + r * D, r < rows, D, t);
+  nz.load(z + r * D, r < rows, D, t);
+  nd.load(dy + r * D, r < rows, D, t);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += stride, r += stride) {
     const bool live = r < rows;
-    float xv[E] = {}, zv[E] = {}, dv[E] = {};
-    if (live) {
-      load_row<TPR, VEC>(x + r * D, D, t, xv);
-      load_row<TPR, VEC>(z + r * D, D, t, zv);
-      load_row<TPR, VEC>(dy + r * D, D, t, dv);
-    }
+    float xv[E], zv[E], dv[E];
+    nx.get(xv);
+    nz.get(zv);
+    nd.get(dv);
+    nx.load(x + (r + stride) * D, r + stride < rows, D, t);
+    nz.load(z + (r + stride) * D, r + stride < rows, D, t);
+    nd.load(dy + (r + stride) * D, r + stride < rows, D, t);
     float s[2] = {0.f, 0.f}, sg[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) {
@@ -203,7 +227,7 @@ gated_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dy, const X* __restrict_
       s[1] = fmaf(dv[e] * wv[e] * (zv[e] * sg[e]), xv[e], s[1]);
     }
     RowSum<TPR, 2>::run(s, sm, slot);
-    const float rs = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float rs = rsqrtf(fmaf(s[0], inv_d, eps));
     const float c = s[1] * inv_d * rs * rs;      // mean(d n) r, the factor of x in n mean(d n)
     if (live) {
       float ox[E], oz[E];
@@ -235,21 +259,26 @@ residual_norm_fwd_kernel(const __nv_bfloat16* __restrict__ y, const H* h, const 
   load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
   if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
   const float inv_d = 1.f / (float)D;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
-    const int64_t r = r0 + rg;
+  Raw<TPR, VEC, __nv_bfloat16> ny;
+  Raw<TPR, VEC, H> nh;
+  const int64_t stride = (int64_t)gridDim.x * RPC;
+  int64_t r = (int64_t)blockIdx.x * RPC + rg;
+  ny.load(y + r * D, r < rows, D, t);
+  nh.load(h + r * D, r < rows, D, t);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += stride, r += stride) {
     const bool live = r < rows;
-    float yv[E] = {}, hv[E] = {};
-    if (live) {
-      load_row<TPR, VEC>(y + r * D, D, t, yv);
-      load_row<TPR, VEC>(h + r * D, D, t, hv);
-    }
+    float yv[E], hv[E];
+    ny.get(yv);
+    nh.get(hv);
+    ny.load(y + (r + stride) * D, r + stride < rows, D, t);
+    nh.load(h + (r + stride) * D, r + stride < rows, D, t);
     float ry = 1.f;
     if (POST) {
       float s[1] = {0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
       RowSum<TPR, 1>::run(s, sm, slot);
-      ry = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+      ry = rsqrtf(fmaf(s[0], inv_d, eps));
     }
     float s[1] = {0.f};
 #pragma unroll
@@ -258,7 +287,7 @@ residual_norm_fwd_kernel(const __nv_bfloat16* __restrict__ y, const H* h, const 
       s[0] = fmaf(hv[e], hv[e], s[0]);
     }
     RowSum<TPR, 1>::run(s, sm, slot);
-    const float rh = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float rh = rsqrtf(fmaf(s[0], inv_d, eps));
     if (live) {
       store_row<TPR, VEC>(h_out + r * D, D, t, hv);
 #pragma unroll
@@ -272,7 +301,7 @@ residual_norm_fwd_kernel(const __nv_bfloat16* __restrict__ y, const H* h, const 
 //   dh = dh' + r_h (p - m mean(p m)),  e = alpha dh,  dw_pre = sum dx m
 //   POST: dy = r_y (e w_post - n mean(e w_post n)), dw_post = sum e n;  else dy = e
 template <int TPR, bool VEC, bool POST, class H>
-__global__ void __launch_bounds__(threads_of(TPR))
+__global__ void __launch_bounds__(threads_of(TPR), bwd_per_sm(TPR))
 residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
                          const __nv_bfloat16* __restrict__ y, const H* __restrict__ h, const void* __restrict__ w_post,
                          const void* __restrict__ w_pre, int w_bf16, __nv_bfloat16* __restrict__ dy,
@@ -287,23 +316,33 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
   load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
   if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
   const float inv_d = 1.f / (float)D;
-  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += (int64_t)gridDim.x * RPC) {
-    const int64_t r = r0 + rg;
+  Raw<TPR, VEC, __nv_bfloat16> ny, nd;
+  Raw<TPR, VEC, H> nh, ndh;
+  const int64_t stride = (int64_t)gridDim.x * RPC;
+  int64_t r = (int64_t)blockIdx.x * RPC + rg;
+  auto load = [&](int64_t q) {
+    const bool in = q < rows;
+    ny.load(y + q * D, in, D, t);
+    nh.load(h + q * D, in, D, t);
+    nd.load(dx + q * D, in, D, t);
+    ndh.load(dh_out + q * D, in && dh_out, D, t);
+  };
+  load(r);
+  for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += stride, r += stride) {
     const bool live = r < rows;
-    float yv[E] = {}, hv[E] = {}, dv[E] = {}, dhv[E] = {};
-    if (live) {
-      load_row<TPR, VEC>(y + r * D, D, t, yv);
-      load_row<TPR, VEC>(h + r * D, D, t, hv);
-      load_row<TPR, VEC>(dx + r * D, D, t, dv);
-      if (dh_out) load_row<TPR, VEC>(dh_out + r * D, D, t, dhv);
-    }
+    float yv[E], hv[E], dv[E], dhv[E];
+    ny.get(yv);
+    nh.get(hv);
+    nd.get(dv);
+    ndh.get(dhv);
+    load(r + stride);
     float ry = 1.f;
     if (POST) {
       float s[1] = {0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
       RowSum<TPR, 1>::run(s, sm, slot);
-      ry = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+      ry = rsqrtf(fmaf(s[0], inv_d, eps));
     }
     float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -313,7 +352,7 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
       s[1] = fmaf(dv[e] * w1[e], hv[e], s[1]);
     }
     RowSum<TPR, 2>::run(s, sm, slot);
-    const float rh = 1.f / sqrtf(fmaf(s[0], inv_d, eps));
+    const float rh = rsqrtf(fmaf(s[0], inv_d, eps));
     const float c = s[1] * inv_d * rh * rh;
     float q[1] = {0.f};
 #pragma unroll
@@ -379,9 +418,6 @@ int64_t grid_of(int64_t rows, int tpr, int per_sm) {
   const int64_t need = (rows + rpc - 1) / rpc, most = (int64_t)kSMs * per_sm;
   return need < most ? need : most;
 }
-// 64-register kernels: 1024 threads an SM in flight
-int per_sm_of(int tpr) { return 1024 / threads_of(tpr); }
-
 bool vec_ok(int D, std::initializer_list<const void*> ptrs) {
   if (D % 8) return false;
   for (const void* p : ptrs)
@@ -414,7 +450,7 @@ bool norm_dim_ok(int D) { return D >= 1 && D <= kMaxD; }
 
 int64_t norm_bwd_parts(int64_t rows, int D) {
   const int tpr = tpr_of(D);
-  return grid_of(rows, tpr, per_sm_of(tpr));
+  return grid_of(rows, tpr, bwd_per_sm(tpr));
 }
 
 cudaError_t launch_gated_norm_fwd(const void* x, int x_f32, const void* z, const void* w, int w_bf16, void* y,

@@ -81,7 +81,8 @@ def _la_args(q, k, v, g, h0, cu_seqlens, scale, dev):
     N = B
     if cu_seqlens is not None:
         cu_host = _cu_host(cu_seqlens)
-        cu_dev = (cu_seqlens if cu_seqlens.is_cuda else cu_host).to(q.device, torch.int32).contiguous()
+        # from pageable memory: staged before the copy returns, without waiting for the stream
+        cu_dev = (cu_seqlens if cu_seqlens.is_cuda else cu_host).to(q.device, torch.int32, non_blocking=True).contiguous()
         N = cu_host.numel() - 1
     a = LaArgs(_is(q, _BF16, q.shape, dev, "q"), _is(k, _BF16, q.shape, dev, "k"),
                _is(v, _BF16, (B, T, Hv, dv), dev, "v"), _is(g, _F32, (Hv,) if head else (B, T, Hv), dev, "g"),
