@@ -32,6 +32,8 @@ struct DgParams {
 
 // One CTA of 128 threads per (chunk slot, head): thread = token.
 __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
+  dependents_may_start();
+  dependency_wait();
   const int64_t item = blockIdx.x;
   const int Hv = p.gates.Hv, h = (int)(item % Hv);
   const int64_t slot = item / Hv;
@@ -92,6 +94,8 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
 // dg of a fixed decay: the sum over all chunks, 256 threads in a fixed order, in 64 bits
 __global__ void __launch_bounds__(256) la_dg_head_kernel(const float* part, float* dg, int64_t slots, int Hv) {
   __shared__ double red[256];
+  dependents_may_start();
+  dependency_wait();
   const int h = blockIdx.x, t = threadIdx.x;
   double s = 0.;
   for (int64_t i = t; i < slots; i += 256) s += part[i * Hv + h];
@@ -108,6 +112,7 @@ __global__ void __launch_bounds__(256) la_dg_head_kernel(const float* part, floa
 __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, const float* x1, __nv_bfloat16* y0,
                                                            __nv_bfloat16* y1, int64_t quads, int G, int D4) {
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  dependency_wait();
   if (i >= quads) return;
   const float4* x = reinterpret_cast<const float4*>(blockIdx.y ? x1 : x0);
   const int64_t row = i / D4, d = i % D4;
@@ -173,7 +178,7 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
   StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
              nullptr, nullptr};
   // o reads h0 through the states alone, so hT may be h0
-  if ((e = launch_states(p, s, status, stream)) != cudaSuccess) return e;
+  if ((e = launch_states(p, s, status, false, stream)) != cudaSuccess) return e;
   // tiles k, q, v | S
   OutRun o{{p.q, p.k, p.v, nullptr}, {base + l.S, nullptr}, {1, 1}, 3, {1, 0, 2, 0}, 1, {0}, {0}, {}, 1};
   o.role[0] = {1, 0, 2, -1, 0, 1, 0x17, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
@@ -193,9 +198,9 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
   StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr};
-  if ((e = launch_states(p, f, status, stream)) != cudaSuccess) return e;
+  if ((e = launch_states(p, f, status, false, stream)) != cudaSuccess) return e;
   StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec, base + l.S, edge};
-  if ((e = launch_states(p, b, status, stream)) != cudaSuccess) return e;
+  if ((e = launch_states(p, b, status, true, stream)) != cudaSuccess) return e;
   if (tokens == 0 || items == 0)
     return p.head_decay ? cudaMemsetAsync(gr.dg, 0, (size_t)p.Hv * 4, stream) : cudaSuccess;
   // tiles v, q, k, do | S hi, lo, dS hi, lo
@@ -206,17 +211,16 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
   DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, tokens * p.Hv, edge, edge_parts(p),
              p.head_decay ? (float*)(base + l.item) : gr.dg};
-  la_dg_kernel<<<(unsigned)items, kC, 0, stream>>>(d);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if ((e = launch(true, la_dg_kernel, dim3((unsigned)items), kC, 0, stream, d)) != cudaSuccess) return e;
   if (p.head_decay) {
-    la_dg_head_kernel<<<(unsigned)p.Hv, 256, 0, stream>>>((const float*)(base + l.item), gr.dg, la_slots(p), p.Hv);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch(true, la_dg_head_kernel, dim3((unsigned)p.Hv), 256, 0, stream, (const float*)(base + l.item), gr.dg,
+                    la_slots(p), p.Hv)) != cudaSuccess)
+      return e;
   }
   if (G > 1) {
     const int64_t quads = tokens * p.Hqk * (p.dk / 4);
-    la_group_sum_kernel<<<dim3((unsigned)((quads + 255) / 256), 2), 256, 0, stream>>>(
-        pq, pk, (__nv_bfloat16*)gr.dq, (__nv_bfloat16*)gr.dk, quads, G, p.dk / 4);
-    e = cudaGetLastError();
+    e = launch(true, la_group_sum_kernel, dim3((unsigned)((quads + 255) / 256), 2), 256, 0, stream, (const float*)pq,
+               (const float*)pk, (__nv_bfloat16*)gr.dq, (__nv_bfloat16*)gr.dk, quads, G, p.dk / 4);
   }
   return e;
 }

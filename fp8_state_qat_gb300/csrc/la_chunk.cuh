@@ -178,6 +178,29 @@ inline cudaError_t allow_smem(K kernel, uint32_t bytes, std::atomic<uint64_t>& d
   return e;
 }
 
+// Programmatic dependent launch: a kernel's CTAs may start, and set themselves up, while the last CTAs of
+// the kernel before it still run; whatever reads or overwrites that kernel's memory comes after
+// dependency_wait(), which every kernel of a chain executes in each of its CTAs, so that its own end also
+// stands for the end of all before it.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependents_may_start() { asm volatile("griddepcontrol.launch_dependents;"); }
+
+template <class... P, class... A>
+inline cudaError_t launch(bool dependent, void (*kernel)(P...), dim3 grid, int threads, uint32_t smem,
+                          cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ---- launchers of the parts (la_state.cu, la_out.cu) ----
 // States at chunk boundaries, bf16 terms per item = slot * Hv + h: [term][dv / 64][dk][64].
 struct StateRun {
@@ -196,7 +219,8 @@ struct StateRun {
 };
 int edge_parts(const LaProblem& p);
 int state_segments(const LaProblem& p);
-cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream);
+// dependent: the launch before it in the stream is one of these kernels
+cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream);
 
 // One family of outputs: out_t = f_in sum_s decay(t, s) (a_t . b_s) c_s + f_st decay_t a_t^T St,
 // s <= t with the state before the chunk (reverse 0), or s >= t with the state after it (reverse 1).

@@ -151,6 +151,10 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
   tc::tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
+  dependents_may_start();
+  // the token tiles and gates are the call's own inputs, so their first ones are fetched during the walks; the
+  // states, all that is written, and every wait for another warp come after
+  if (tid != 0 && warp != 2) dependency_wait();
 
   if (tid == 0 || tid == 96) {
     // ---- loads: thread 0 the token tiles, thread 96 the state tiles, each as its slot falls free ----
@@ -165,6 +169,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       if (!locate(p, i, it)) continue;
 #pragma unroll 1
       for (int j = 0; j < per; ++j) {
+        if (toks && x == kTok) dependency_wait();
         if (!(ok = wait(sh.dead, empty[slot], turn ^ 1))) break;
         const uint32_t dst = base + slot * kTile, bar = tc::smem_u32(&full[slot]);
         if (toks) {
@@ -200,6 +205,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
     while (true) {
       const bool more = i < items;
       const uint32_t s = k % kEntries;
+      if (k == kEntries) dependency_wait();
       ok = wait(sh.dead, sh.gempty[s], ((k / kEntries) & 1) ^ 1);
       if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
       Entry& e = entries[s];
@@ -611,8 +617,7 @@ cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cud
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(la_out_kernel, kSmemBytes, allowed);
   if (e != cudaSuccess) return e;
-  la_out_kernel<<<(unsigned)std::min<int64_t>(items, kSMs), kThreads, kSmemBytes, stream>>>(m, o);
-  return cudaGetLastError();
+  return launch(true, la_out_kernel, dim3((unsigned)std::min<int64_t>(items, kSMs)), kThreads, kSmemBytes, stream, m, o);
 }
 
 }  // namespace la

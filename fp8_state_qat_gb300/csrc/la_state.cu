@@ -89,13 +89,17 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const int row = 32 * quad + lane;        // key channel
   const bool live = row < p.dk;            // dk 64: lanes 64-127 of the product are not used
 
+  dependents_may_start();
   const int tiles = p.dv / NV;
   int u = blockIdx.x;
   const int vt = u % tiles;
   u /= tiles;
   const int seg = u % p.nseg;
   u /= p.nseg;
-  if (p.totals && seg == p.nseg - 1) return;   // nothing follows the last segment
+  if (p.totals && seg == p.nseg - 1) {   // nothing follows the last segment
+    dependency_wait();
+    return;
+  }
   const int Hv = p.gates.Hv;
   const int n = p.sorted ? p.order[u / Hv] : u / Hv, h = u % Hv, unit = n * Hv + h, hq = h / (Hv / p.Hqk);
   const int t0 = (int)p.seqs.start(n), len = (int)p.seqs.len(n), slot0 = (int)p.seqs.slot0(n);
@@ -126,6 +130,9 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   tc::tc_fence_after();
   const uint32_t tmem = sh.tmem;
   bool ok = true;
+  // inputs of the call are read above and below without waiting; what a kernel of this call wrote (the joined
+  // segment states, S) and what it may still read (the workspace) only after
+  dependency_wait();
 
   float s[HC];   // state elements (row, vt NV + part HC + j)
   const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * NV + part * HC;
@@ -381,6 +388,8 @@ __global__ void __launch_bounds__(256) la_join_kernel(float* seg_tot, const floa
                                                       int64_t elems) {
   const int64_t unit = blockIdx.y;
   const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;   // four state elements
+  dependents_may_start();
+  dependency_wait();
   if (e * 4 >= elems) return;
   float4 s = s0 ? reinterpret_cast<const float4*>(s0 + unit * elems)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i = 0; i < nseg; ++i) {
@@ -395,12 +404,12 @@ __global__ void __launch_bounds__(256) la_join_kernel(float* seg_tot, const floa
 constexpr int kSMs = 152;
 
 template <int NV>
-cudaError_t run(const CUtensorMap (&m)[4], const Params& p, int64_t units, cudaStream_t stream) {
+cudaError_t run(const CUtensorMap (&m)[4], const Params& p, int64_t units, bool dependent, cudaStream_t stream) {
   static std::atomic<uint64_t> allowed{0};
   cudaError_t e = allow_smem(la_state_kernel<NV>, smem_bytes<NV>(), allowed);
   if (e != cudaSuccess) return e;
-  la_state_kernel<NV><<<(unsigned)(units * p.nseg * (p.dv / NV)), kThreads, smem_bytes<NV>(), stream>>>(m[0], m[1], m[2], m[3], p);
-  return cudaGetLastError();
+  return launch(dependent, la_state_kernel<NV>, dim3((unsigned)(units * p.nseg * (p.dv / NV))), kThreads, smem_bytes<NV>(),
+                stream, m[0], m[1], m[2], m[3], p);
 }
 
 }  // namespace
@@ -428,7 +437,7 @@ static bool wide_tiles(const LaProblem& p) {
 }
 int edge_parts(const LaProblem& p) { return p.dv / 64 * (kWorkers / 32); }
 
-cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cudaStream_t stream) {
+cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream) {
   const int64_t units = (int64_t)p.N * p.Hv, tokens = (int64_t)p.B * p.T;
   if (units == 0) return cudaSuccess;
   const int64_t elems = (int64_t)p.dk * p.dv;
@@ -457,15 +466,16 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, cu
     });
   }
   const bool wide = wide_tiles(p) && r.terms == 1;
-  auto go = [&] { return wide ? run<128>(m, s, units, stream) : run<64>(m, s, units, stream); };
+  auto go = [&] { return wide ? run<128>(m, s, units, dependent, stream) : run<64>(m, s, units, dependent, stream); };
   if (s.nseg > 1) {
     s.totals = 1;
     s.store = s.other = 0;
     cudaError_t e = go();
     if (e != cudaSuccess) return e;
-    la_join_kernel<<<dim3((unsigned)((elems / 4 + 255) / 256), (unsigned)units), 256, 0, stream>>>(
-        r.seg_tot, r.seg_dec, r.s0, s.nseg, elems);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch(true, la_join_kernel, dim3((unsigned)((elems / 4 + 255) / 256), (unsigned)units), 256, 0, stream, r.seg_tot,
+               (const float*)r.seg_dec, r.s0, s.nseg, elems);
+    if (e != cudaSuccess) return e;
+    dependent = true;
     s.totals = 0;
     s.store = r.states != nullptr;
     s.other = r.other != nullptr;
