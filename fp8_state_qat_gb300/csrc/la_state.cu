@@ -1,17 +1,17 @@
 // la_state.cu -- the states at the chunk boundaries of linear attention with a decay for each head.
 //
-// Per sequence, value head and 64 (or 128) value columns, over 128-token chunks:
+// Per sequence, value head and 64 value columns, over 128-token chunks:
 //   forwards  S <- Gam S + sum_i w_i k_i v_i^T,  w_i = exp(gam_C - gam_i),  Gam = exp(gam_C)
 //   backwards dS <- Gam dS + sum_t w_t q_t do_t^T,  w_t = scale exp(gam_t),  chunks last to first
 // and the state before each chunk's contribution is stored for the output kernel.
 //
-// The contributions do not depend on the state: each is one tcgen05 product [dk x 128] [128 x NV] into
-// a fresh accumulator, and the walk itself is one fp32 multiply-add per state element, held in
-// registers. The weights go to the K side, as the A operand in tensor memory: thread = key channel
-// reads its column of the K tile, and w_i k_i (fp32) is written as three bf16 terms (24 bits, so the
-// state has fp32 accuracy; two terms leave 2^-17 of it), the A terms of chunk c + 1 while the products of
-// chunk c run. That splitting is what the kernel spends its time on (about 7 instructions per K element and
-// value tile), so 16 warps do it. V stays as TMA left it (MN-major B operand).
+// The contributions do not depend on the state: each is one tcgen05 product [dk x 128] [128 x 64] into a
+// fresh accumulator, and the walk itself is one fp32 multiply-add per state element, held in registers.
+// K stays as TMA left it (MN-major A operand). The weights go to the V side: w_i v_i (fp32) is written as
+// three bf16 terms (24 bits, so the state has fp32 accuracy; two terms leave 2^-17 of it), in V's own
+// swizzled places, so that a thread moves 16 bytes at a time and nothing is transposed. (Weighting K instead,
+// through tensor memory, takes a 16-bit load an element and twice the elements: 64 us against the figures below.)
+// The terms of chunk c + 1 are written while the products of chunk c run.
 // Tail rows of a partial chunk belong to another sequence, so they are zeroed, not just weighted by zero.
 //
 // Few sequences and heads: each walk is cut into segments, a first launch computes every segment's
@@ -27,9 +27,11 @@ namespace la {
 namespace {
 
 constexpr int kWorkers = 512, kThreads = kWorkers + 96;
-constexpr int kStages = 3;
-constexpr uint32_t TM_A = 0, TM_ACC = 384;   // two buffers of three 64-column A terms; the accumulator
-constexpr uint32_t kTmemCols = 512;
+constexpr int kNV = 64;                      // value columns of a CTA
+constexpr int kHC = kNV / 4;                 // of a thread
+constexpr uint32_t kTmemCols = 128;          // two accumulators
+// shared memory: two K tiles, two V tiles, one or two sets of V's terms, the states on their way out, S
+constexpr uint32_t kOffV = 2 * kTile, kOffTerm = kOffV + 2 * kBlk, kTermSet = 3 * kBlk;
 
 struct Params {
   Seqs seqs;
@@ -42,44 +44,54 @@ struct Params {
   int Hqk, dk, dv, terms, reverse, nseg;
   int totals;       // this launch computes the segments' contributions
   int store, other; // the states are stored; <S, state> is computed
+  int sets;         // of V's terms: 2, or 1 where S needs the room
   float scale;
   int sorted;
   uint8_t order[64];   // the sequences, longest first
 };
-
-template <int NV>
-constexpr uint32_t stage_bytes() { return kTile + NV / 64 * kBlk; }
-template <int NV>
-constexpr uint32_t off_stage() { return kStages * stage_bytes<NV>(); }   // states on their way out: 32 KB
-template <int NV>
-constexpr uint32_t off_other() { return off_stage<NV>() + kTile; }         // S of the chunk, hi and lo (NV 64)
-template <int NV>
-constexpr uint32_t smem_bytes() { return off_other<NV>() + (NV == 64 ? kTile : 0) + 1024; }
+__host__ __device__ inline uint32_t off_out(const Params& p) { return kOffTerm + p.sets * kTermSet; }
+__host__ __device__ inline uint32_t off_other(const Params& p) { return off_out(p) + (p.store ? p.terms * kBlk : 0); }
+inline uint32_t smem_bytes(const Params& p) { return off_other(p) + (p.other ? 2 * kBlk : 0) + 1024; }
+constexpr uint32_t kMaxSmem = kOffTerm + 2 * kTermSet + 2 * kBlk + 1024;
 
 struct Shared {
-  uint64_t full[kStages];   // a step's tiles have landed
-  uint64_t wready[2];       // its weights are written
-  uint64_t wfree[2];        // and read
-  uint64_t aready;          // its A terms are written and the accumulator of the step before is read
-  uint64_t mma;             // its product is complete
-  uint64_t sfree;           // the states written out are read from shared memory
-  uint64_t ofull, oread;    // S of the step has landed; is read
+  uint64_t kfull[2], vfull[2];   // a step's tiles have landed
+  uint64_t wready[2], wfree[2];  // its weights are written; are read
+  uint64_t aready[2];            // its terms are written (and V is read)
+  uint64_t mma[2];               // its product is complete
+  uint64_t sready, sfree;        // the state is laid out for its way out; has been read from there
+  uint64_t ofull, oread;         // S of the step has landed; is read
   uint32_t tmem;
   int dead;
-  float decay[2], log_decay[2];   // Gam of a step; log Gam of the whole segment, in two parts
-  __align__(16) float w[2][kC];   // read and written 16 bytes at a time
+  float decay[2], log_decay[2];  // Gam of a step; log Gam of the whole segment, in two parts
+  __align__(16) float w[2][kC];
 };
 
-// Warps 0-15 weight K and hold the state; warp 16 loads and issues the products; warps 17
-// and 18 compute the weights, of every other step each: the latency of a step's loads and sums is longer than
-// the step.
-template <int NV>
+// 8 values -> three bf16 terms each
+__device__ __forceinline__ void split3(const float2 (&x)[4], uint4& t1, uint4& t2, uint4& t3) {
+  const float2 neg = make_float2(-1.f, -1.f);
+  uint32_t a[4], b[4], c[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    a[i] = pack_bf16(x[i].x, x[i].y);
+    const float2 y = __ffma2_rn(unpack_bf16(a[i]), neg, x[i]);
+    b[i] = pack_bf16(y.x, y.y);
+    const float2 z = __ffma2_rn(unpack_bf16(b[i]), neg, y);
+    c[i] = pack_bf16(z.x, z.y);
+  }
+  t1 = make_uint4(a[0], a[1], a[2], a[3]);
+  t2 = make_uint4(b[0], b[1], b[2], b[3]);
+  t3 = make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// Warps 0-15 weight V and hold the state; warp 16 loads and issues the products; warps 17 and 18 compute the
+// weights, of every other step each: the latency of a step's loads and sums is longer than the step.
 __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
-                const __grid_constant__ CUtensorMap ts, const __grid_constant__ CUtensorMap to, const Params p) {
+                const __grid_constant__ CUtensorMap ts, const __grid_constant__ CUtensorMap to,
+                const __grid_constant__ Params p) {
   extern __shared__ unsigned char smem_raw[];
   __shared__ __align__(16) Shared sh;
-  constexpr int HC = NV / 4;   // value columns a thread
   const uint32_t raw = tc::smem_u32(smem_raw);
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (sbase - raw);
@@ -90,7 +102,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const bool live = row < p.dk;            // dk 64: lanes 64-127 of the product are not used
 
   dependents_may_start();
-  const int tiles = p.dv / NV;
+  const int tiles = p.dv / kNV;
   int u = blockIdx.x;
   const int vt = u % tiles;
   u /= tiles;
@@ -111,13 +123,15 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   auto rows_of = [&](int c) { return min(kC, len - c * kC); };
 
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) tc::mbar_init(tc::smem_u32(&sh.full[i]), 1);
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.kfull[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.vfull[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
       tc::mbar_init(tc::smem_u32(&sh.wfree[i]), kWorkers / 32);
+      tc::mbar_init(tc::smem_u32(&sh.aready[i]), kWorkers / 32);
+      tc::mbar_init(tc::smem_u32(&sh.mma[i]), 1);
     }
-    tc::mbar_init(tc::smem_u32(&sh.aready), kWorkers / 32);
-    tc::mbar_init(tc::smem_u32(&sh.mma), 1);
+    tc::mbar_init(tc::smem_u32(&sh.sready), kWorkers / 32);
     tc::mbar_init(tc::smem_u32(&sh.sfree), 1);
     tc::mbar_init(tc::smem_u32(&sh.ofull), 1);
     tc::mbar_init(tc::smem_u32(&sh.oread), kWorkers / 32);
@@ -134,61 +148,68 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   // segment states, S) and what it may still read (the workspace) only after
   dependency_wait();
 
-  float s[HC];   // state elements (row, vt NV + part HC + j)
-  const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * NV + part * HC;
-  const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * NV + part * HC;
-  float log_decay = 0.f;   // of this warp's steps (warps 17, 18)
+  float s[kHC];   // state elements (row, vt kNV + part kHC + j)
+  const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * kNV + part * kHC;
+  const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * kNV + part * kHC;
 
   if (warp == kWorkers / 32) {
-    const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, NV, false, true);
-    int loaded = 0;
-    auto load = [&](int i) {
-      const uint32_t bar = tc::smem_u32(&sh.full[i % kStages]), dst = sbase + (i % kStages) * stage_bytes<NV>();
-      const int tok = t0 + chunk_of(i) * kC;
-      tc::mbar_expect_tx(bar, p.dk / 64 * kBlk + NV / 64 * kBlk);
-      for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, tok);
-      for (int b = 0; b < NV / 64; ++b) tc::tma_load_3d(dst + kTile + b * kBlk, &ty, bar, vt * NV + 64 * b, h, tok);
+    // ---- loads and products ----
+    constexpr uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, kNV, true, true);
+    auto token = [&](int i) { return t0 + chunk_of(i) * kC; };
+    auto load_k = [&](int i) {
+      const uint32_t bar = tc::smem_u32(&sh.kfull[i & 1]), dst = sbase + (i & 1) * kTile;
+      tc::mbar_expect_tx(bar, p.dk / 64 * kBlk);
+      for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, token(i));
+    };
+    auto load_v = [&](int i) {
+      const uint32_t bar = tc::smem_u32(&sh.vfull[i & 1]);
+      tc::mbar_expect_tx(bar, kBlk);
+      tc::tma_load_3d(sbase + kOffV + (i & 1) * kBlk, &ty, bar, vt * kNV, h, token(i));
     };
     auto state_row = [&](int i, int terms, int term) {   // of the stored states: this value tile's rows
       const int item = (slot0 + chunk_of(i)) * Hv + h;
-      return ((item * terms + term) * (p.dv / 64) + vt * (NV / 64)) * p.dk;
+      return ((item * terms + term) * tiles + vt) * p.dk;
     };
     auto load_other = [&](int i) {
       tc::mbar_expect_tx(tc::smem_u32(&sh.ofull), 2 * p.dk * 128);
       for (int t = 0; t < 2; ++t)
-        tc::tma_load_2d(sbase + off_other<NV>() + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
+        tc::tma_load_2d(sbase + off_other(p) + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
     };
-    for (; loaded < min(2, steps); ++loaded)
-      if (lane == 0) load(loaded);
-    int others = 0;
-    if (p.other && steps) {
-      if (lane == 0) load_other(0);
-      others = 1;
+    int ks = min(2, steps), vs = ks, os = p.other && steps ? 1 : 0, issued = 0;   // loads and products issued
+    if (lane == 0) {
+      for (int i = 0; i < vs; ++i) {
+        load_v(i);
+        load_k(i);
+      }
+      if (os) load_other(0);
     }
+    __syncwarp();
     const uint32_t me = elect_one();
-    int issued = 0;
+#pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-      ok = wait(sh.dead, sh.aready, i & 1);
+      const uint32_t turn = (i >> 1) & 1;
+      ok = wait(sh.dead, sh.aready[i & 1], turn) && wait(sh.dead, sh.kfull[i & 1], turn);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
-      const uint64_t bd = tc::make_sdesc(sbase + (i % kStages) * stage_bytes<NV>() + kTile, kBlk, 1024);
-      const uint32_t a = tmem + TM_A + (i & 1) * 192;
+      const uint64_t ad = tc::make_sdesc(sbase + (i & 1) * kTile, kBlk, 1024);
+      const uint64_t bd = tc::make_sdesc(sbase + kOffTerm + (p.sets == 2 ? (i & 1) * kTermSet : 0), kBlk, 1024);
 #pragma unroll
       for (int t = 0; t < 3; ++t)
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ta(tmem + TM_ACC, a + 64 * t + 8 * ks, dadv(bd, ks * 2048), idesc, t + ks > 0, me);
-      mma_commit_w(tc::smem_u32(&sh.mma), me);
+        for (int k = 0; k < 8; ++k)
+          mma_bf16_w(tmem + (i & 1) * kNV, dadv(ad, k * 2048), dadv(bd, t * kBlk + k * 2048), idesc, t + k > 0, me);
+      mma_commit_w(tc::smem_u32(&sh.mma[i & 1]), me);
       issued = i + 1;
-      if (i + 2 < steps) {   // its stage held step i - 1, whose product the workers have taken
-        if (lane == 0) load(i + 2);
-        ++loaded;
+      if (i + 2 < steps) {   // V of this step is weighted
+        if (lane == 0) load_v(i + 2);
+        ++vs;
       }
       if (p.store) {
+        ok = wait(sh.dead, sh.sready, i & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (lane == 0) {
-          for (int b = 0; b < (NV == 64 ? p.terms : 2); ++b)
-            tc::tma_store_2d(&ts, sbase + off_stage<NV>() + b * kBlk, 0,
-                             NV == 64 ? state_row(i, p.terms, b) : state_row(i, 1, 0) + b * p.dk);
+          for (int t = 0; t < p.terms; ++t)
+            tc::tma_store_2d(&ts, sbase + off_out(p) + t * kBlk, 0, state_row(i, p.terms, t));
           tc::bulk_commit();
         }
         __syncwarp();
@@ -197,7 +218,13 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         ok = wait(sh.dead, sh.oread, i & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (lane == 0) load_other(i + 1);
-        ++others;
+        ++os;
+      }
+      if (i + 2 < steps) {   // K of this step is free when its product is complete
+        ok = wait(sh.dead, sh.mma[i & 1], turn);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) load_k(i + 2);
+        ++ks;
       }
       if (p.store && lane == 0) {
         tc::bulk_wait_read();
@@ -206,15 +233,16 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       __syncwarp();
     }
     if (lane == 0 && !ok) {   // nothing of this CTA is in flight when it ends
-      for (int i = max(0, loaded - kStages); i < loaded; ++i)
-        tc::mbar_wait(tc::smem_u32(&sh.full[i % kStages]), (i / kStages) & 1, 1u << 22);
-      if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma), (issued - 1) & 1, 1u << 22);
-      if (others) tc::mbar_wait(tc::smem_u32(&sh.ofull), (others - 1) & 1, 1u << 22);
+      for (int i = max(0, ks - 2); i < ks; ++i) tc::mbar_wait(tc::smem_u32(&sh.kfull[i & 1]), (i >> 1) & 1, 1u << 22);
+      for (int i = max(0, vs - 2); i < vs; ++i) tc::mbar_wait(tc::smem_u32(&sh.vfull[i & 1]), (i >> 1) & 1, 1u << 22);
+      if (os) tc::mbar_wait(tc::smem_u32(&sh.ofull), (os - 1) & 1, 1u << 22);
+      if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma[(issued - 1) & 1]), ((issued - 1) >> 1) & 1, 1u << 22);
       tc::bulk_wait_read();
     }
   } else if (warp > kWorkers / 32) {
+    // ---- weights ----
     const int which = warp - kWorkers / 32 - 1;
-    float gx[4];
+    float gx[4], log_decay = 0.f;   // of this warp's steps
     auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
     if (which < steps) gates(which);
     for (int i = which; i < steps; i += 2) {
@@ -237,114 +265,100 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     }
     if (lane == 0) sh.log_decay[which] = log_decay;
   } else {
+    // ---- the state ----
     const float* src = p.totals ? nullptr : p.nseg > 1 ? p.seg_tot + seg_g : p.s0 ? p.s0 + sbase_g : nullptr;
 #pragma unroll
-    for (int j = 0; j < HC; j += 4) {
+    for (int j = 0; j < kHC; j += 4) {
       const float4 v = src && live ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
       s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
     }
-    // byte offsets of this channel within an 8-row group of the swizzled tile
-    uint32_t off[8];
-#pragma unroll
-    for (int r = 0; r < 8; ++r) off[r] = (row >> 6) * kBlk + part * 4096 + tc::sw128(r, (row & 63) * 2);
     const bool work = 32 * quad < p.dk;   // uniform in the warp
     float decay = 1.f;                    // Gam of the chunk whose product is in flight
     auto take = [&](int i) {              // the product of step i -> the state
-      ok = wait(sh.dead, sh.mma, i & 1);
+      ok = ok && wait(sh.dead, sh.mma[i & 1], (i >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       tc::tc_fence_after();
       if (!work) return;
-      float v[HC];
-#pragma unroll
-      for (int q = 0; q < HC; q += 16) tc::tmem_ld16(tc::tmem_addr(tmem, lane0, TM_ACC + part * HC + q), v + q);
+      float v[kHC];
+      tc::tmem_ld16(tc::tmem_addr(tmem, lane0, (i & 1) * kNV + part * kHC), v);
       tc::tmem_ld_wait();
       const float2 d2 = make_float2(decay, decay);
 #pragma unroll
-      for (int j = 0; j < HC; j += 2) {
+      for (int j = 0; j < kHC; j += 2) {
         const float2 r = __ffma2_rn(d2, make_float2(s[j], s[j + 1]), make_float2(v[j], v[j + 1]));
         s[j] = r.x;
         s[j + 1] = r.y;
       }
     };
-    const float2 neg = make_float2(-1.f, -1.f);
+    // this thread's 16-byte pieces of V and its terms: rows tid / 8 and 64 more, piece tid % 8
+    const int vrow = tid >> 3;
+    const uint32_t voff = tc::sw128(vrow, (tid & 7) * 16);
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const int c = chunk_of(i), L = rows_of(c);
-      unsigned char* kt = sm + (i % kStages) * stage_bytes<NV>();
-      ok = wait(sh.dead, sh.full[i % kStages], (i / kStages) & 1) && wait(sh.dead, sh.wready[i & 1], (i >> 1) & 1);
-      if (L < kC) {   // uniform: the tail rows are another sequence's. K: what this warp reads; V: the product
-        const int r = 32 * part + lane;
-        if (r >= L) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            *reinterpret_cast<uint4*>(kt + (quad >> 1) * kBlk + tc::sw128(r, (quad & 1) * 64 + 16 * b)) = make_uint4(0, 0, 0, 0);
-        }
-        __syncwarp();
-        zero_tail_rows(kt + kTile, NV / 64, tid, L);
-        tc::fence_proxy_async_smem();
-      }
+      if (p.sets == 1 && i > 0) take(i - 1);   // its terms give way
+      ok = ok && wait(sh.dead, sh.vfull[i & 1], (i >> 1) & 1) && wait(sh.dead, sh.wready[i & 1], (i >> 1) & 1);
       const float decay_i = sh.decay[i & 1];
-      if (work) {
-        const float* ws = sh.w[i & 1] + 32 * part;
-        uint32_t t1[16], t2[16], t3[16];
+      {
+        const unsigned char* v = sm + kOffV + (i & 1) * kBlk + voff;
+        unsigned char* t = sm + kOffTerm + (p.sets == 2 ? (i & 1) * kTermSet : 0) + voff;
 #pragma unroll
-        for (int q = 0; q < 16; q += 2) {
-          const unsigned char* g8 = kt + (q >> 2) * 1024;
-          const float4 wv = *reinterpret_cast<const float4*>(ws + 2 * q);
-          const float2 w2[2] = {make_float2(wv.x, wv.y), make_float2(wv.z, wv.w)};
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int o = q + e;
-            const uint32_t k0 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * o) & 7]);
-            const uint32_t k1 = *reinterpret_cast<const uint16_t*>(g8 + off[(2 * o + 1) & 7]);
-            const float2 x = __fmul2_rn(make_float2(__uint_as_float(k0 << 16), __uint_as_float(k1 << 16)), w2[e]);
-            t1[o] = pack_bf16(x.x, x.y);
-            const float2 y = __ffma2_rn(unpack_bf16(t1[o]), neg, x);
-            t2[o] = pack_bf16(y.x, y.y);
-            const float2 z = __ffma2_rn(unpack_bf16(t2[o]), neg, y);
-            t3[o] = pack_bf16(z.x, z.y);
-          }
+        for (int e = 0; e < 2; ++e) {
+          const float w = sh.w[i & 1][vrow + 64 * e];
+          uint4 q = *reinterpret_cast<const uint4*>(v + 8192 * e);
+          if (vrow + 64 * e >= L) q = make_uint4(0, 0, 0, 0);   // another sequence's
+          const float2 w2 = make_float2(w, w);
+          const float2 x[4] = {__fmul2_rn(unpack_bf16(q.x), w2), __fmul2_rn(unpack_bf16(q.y), w2),
+                               __fmul2_rn(unpack_bf16(q.z), w2), __fmul2_rn(unpack_bf16(q.w), w2)};
+          uint4 t1, t2, t3;
+          split3(x, t1, t2, t3);
+          *reinterpret_cast<uint4*>(t + 8192 * e) = t1;
+          *reinterpret_cast<uint4*>(t + 8192 * e + kBlk) = t2;
+          *reinterpret_cast<uint4*>(t + 8192 * e + 2 * kBlk) = t3;
         }
-        const uint32_t at = TM_A + (i & 1) * 192 + 16 * part;
-        tmem_st16u(tc::tmem_addr(tmem, lane0, at), t1);
-        tmem_st16u(tc::tmem_addr(tmem, lane0, at + 64), t2);
-        tmem_st16u(tc::tmem_addr(tmem, lane0, at + 128), t3);
-        tc::tmem_st_wait();
       }
-      if (i > 0) take(i - 1);
-      if (p.store && i > 0) ok = ok && wait(sh.dead, sh.sfree, (i - 1) & 1);
+      if (L < kC) {   // uniform: K's tail rows would meet zero weights, but not with a NaN
+        ok = ok && wait(sh.dead, sh.kfull[i & 1], (i >> 1) & 1);
+        zero_tail_rows(sm + (i & 1) * kTile, p.dk / 64, tid, L);
+      }
+      tc::fence_proxy_async_smem();
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      if (p.store && live) {   // the state before this chunk, 128-byte swizzled rows of 64 columns
-#pragma unroll
-        for (int j = 0; j < HC; j += 8) {
-          const int col = part * HC + j;
-          unsigned char* at = sm + off_stage<NV>() + (col / 64) * kBlk + tc::sw128(row, (col % 64) * 2);
-          if (NV == 64 && p.terms == 2) {
-            uint4 hi, lo;
-            split8(s + j, hi, lo);
-            *reinterpret_cast<uint4*>(at) = hi;
-            *reinterpret_cast<uint4*>(at + kBlk) = lo;
-          } else {
-            *reinterpret_cast<uint4*>(at) = pack8(s + j);
-          }
-        }
-        tc::fence_proxy_async_smem();
-      }
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         tc::mbar_arrive(tc::smem_u32(&sh.wfree[i & 1]));
-        tc::mbar_arrive(tc::smem_u32(&sh.aready));
+        tc::mbar_arrive(tc::smem_u32(&sh.aready[i & 1]));
       }
-      decay = decay_i;
-      if (NV == 64 && p.other) {
-        ok = wait(sh.dead, sh.ofull, i & 1);
+      if (p.sets == 2 && i > 0) take(i - 1);
+      if (p.store) {   // the state before this chunk, as 128-byte swizzled rows of 64 columns
+        if (i > 0) ok = ok && wait(sh.dead, sh.sfree, (i - 1) & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < kHC; j += 8) {
+            unsigned char* at = sm + off_out(p) + tc::sw128(row, (part * kHC + j) * 2);
+            if (p.terms == 2) {
+              uint4 hi, lo;
+              split8(s + j, hi, lo);
+              *reinterpret_cast<uint4*>(at) = hi;
+              *reinterpret_cast<uint4*>(at + kBlk) = lo;
+            } else {
+              *reinterpret_cast<uint4*>(at) = pack8(s + j);
+            }
+          }
+          tc::fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.sready));
+      }
+      if (p.other) {
+        ok = ok && wait(sh.dead, sh.ofull, i & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         float2 x = make_float2(0.f, 0.f);
         if (live) {
 #pragma unroll
-          for (int j = 0; j < HC; j += 8) {
-            const unsigned char* at = sm + off_other<NV>() + tc::sw128(row, (part * HC + j) * 2);
+          for (int j = 0; j < kHC; j += 8) {
+            const unsigned char* at = sm + off_other(p) + tc::sw128(row, (part * kHC + j) * 2);
             const uint4 hv = *reinterpret_cast<const uint4*>(at), lv = *reinterpret_cast<const uint4*>(at + kBlk);
             const uint32_t hu[4] = {hv.x, hv.y, hv.z, hv.w}, lu[4] = {lv.x, lv.y, lv.z, lv.w};
 #pragma unroll
@@ -359,6 +373,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         if (lane == 0)
           p.edge[(((int64_t)(slot0 + c) * Hv + h) * tiles + vt) * (kWorkers / 32) + warp] = decay_i * sum;
       }
+      decay = decay_i;
     }
     if (ok && steps) take(steps - 1);
   }
@@ -380,37 +395,38 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   float* dst = p.totals ? p.seg_tot + seg_g : p.sT && seg == p.nseg - 1 ? p.sT + sbase_g : nullptr;
   if (dst && live)
 #pragma unroll
-    for (int j = 0; j < HC; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
+    for (int j = 0; j < kHC; j += 4) *reinterpret_cast<float4*>(dst + j) = make_float4(s[j], s[j + 1], s[j + 2], s[j + 3]);
 }
 
-// Segment contributions -> the state that each segment starts from (in place), element by element.
+// Segment contributions -> the state that each segment starts from (in place), element by element; eight
+// segments' loads are in flight at a time.
 __global__ void __launch_bounds__(256) la_join_kernel(float* seg_tot, const float* seg_dec, const float* s0, int nseg,
-                                                      int64_t elems) {
+                                                      int elems) {
   const int64_t unit = blockIdx.y;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;   // four state elements
+  const int e = blockIdx.x * 256 + threadIdx.x;
   dependents_may_start();
   dependency_wait();
-  if (e * 4 >= elems) return;
-  float4 s = s0 ? reinterpret_cast<const float4*>(s0 + unit * elems)[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < nseg; ++i) {
-    float4* at = reinterpret_cast<float4*>(seg_tot + (unit * nseg + i) * elems) + e;
-    const float d = seg_dec[unit * nseg + i];
-    const float4 x = i + 1 < nseg ? *at : make_float4(0.f, 0.f, 0.f, 0.f);
-    *at = s;
-    s = make_float4(fmaf(d, s.x, x.x), fmaf(d, s.y, x.y), fmaf(d, s.z, x.z), fmaf(d, s.w, x.w));
+  if (e >= elems) return;
+  float s = s0 ? s0[unit * elems + e] : 0.f;
+  float* at = seg_tot + unit * nseg * elems + e;
+  const float* dec = seg_dec + unit * nseg;
+  for (int i0 = 0; i0 < nseg; i0 += 8) {
+    float x[8], d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {   // the last segment's contribution is not computed, nor needed
+      x[j] = i0 + j + 1 < nseg ? at[(int64_t)(i0 + j) * elems] : 0.f;
+      d[j] = i0 + j + 1 < nseg ? dec[i0 + j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j < nseg) {
+        at[(int64_t)(i0 + j) * elems] = s;
+        s = fmaf(d[j], s, x[j]);
+      }
   }
 }
 
 constexpr int kSMs = 152;
-
-template <int NV>
-cudaError_t run(const CUtensorMap (&m)[4], const Params& p, int64_t units, bool dependent, cudaStream_t stream) {
-  static std::atomic<uint64_t> allowed{0};
-  cudaError_t e = allow_smem(la_state_kernel<NV>, smem_bytes<NV>(), allowed);
-  if (e != cudaSuccess) return e;
-  return launch(dependent, la_state_kernel<NV>, dim3((unsigned)(units * p.nseg * (p.dv / NV))), kThreads, smem_bytes<NV>(),
-                stream, m[0], m[1], m[2], m[3], p);
-}
 
 }  // namespace
 
@@ -430,12 +446,7 @@ int state_segments(const LaProblem& p) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kSMs / walks, chunks / 4));
 }
 
-// A tile of 128 value columns weights K once for both halves, but has half as many CTAs and no room in
-// shared memory for second terms.
-static bool wide_tiles(const LaProblem& p) {
-  return p.dv == 128 && (int64_t)p.N * p.Hv * state_segments(p) >= kSMs;
-}
-int edge_parts(const LaProblem& p) { return p.dv / 64 * (kWorkers / 32); }
+int edge_parts(const LaProblem& p) { return p.dv / kNV * (kWorkers / 32); }
 
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream) {
   const int64_t units = (int64_t)p.N * p.Hv, tokens = (int64_t)p.B * p.T;
@@ -455,25 +466,30 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bo
   if (r.other && !make_bf16_rows_map(&m[3], r.other, rows * 2, p.dk)) return cudaErrorNotSupported;
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
            status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
-           r.scale};
+           r.other ? 1 : 2, r.scale};
   // Walks of unequal lengths: the longest first, so that the last ones to start are short (b = 1, 8 packed
-  // sequences of 1 to 8192 tokens, 32 heads: 200 -> 177 us). Many sequences even out by themselves.
+  // sequences of 1 to 8192 tokens, 32 heads: an eighth of the time). Many sequences even out by themselves.
   if (p.cu_host && p.N <= 64) {
     s.sorted = 1;
     for (int i = 0; i < p.N; ++i) s.order[i] = (uint8_t)i;
-    std::stable_sort(s.order, s.order + p.N, [&](uint8_t a, uint8_t b) {
-      return p.cu_host[a + 1] - p.cu_host[a] > p.cu_host[b + 1] - p.cu_host[b];
+    std::sort(s.order, s.order + p.N, [&](uint8_t a, uint8_t b) {
+      const int32_t x = p.cu_host[a + 1] - p.cu_host[a], y = p.cu_host[b + 1] - p.cu_host[b];
+      return x != y ? x > y : a < b;
     });
   }
-  const bool wide = wide_tiles(p) && r.terms == 1;
-  auto go = [&] { return wide ? run<128>(m, s, units, dependent, stream) : run<64>(m, s, units, dependent, stream); };
+  static std::atomic<uint64_t> allowed{0};
+  cudaError_t e = allow_smem(la_state_kernel, kMaxSmem, allowed);
+  if (e != cudaSuccess) return e;
+  auto go = [&] {
+    return launch(dependent, la_state_kernel, dim3((unsigned)(units * s.nseg * (p.dv / kNV))), kThreads, smem_bytes(s),
+                  stream, m[0], m[1], m[2], m[3], s);
+  };
   if (s.nseg > 1) {
     s.totals = 1;
     s.store = s.other = 0;
-    cudaError_t e = go();
-    if (e != cudaSuccess) return e;
-    e = launch(true, la_join_kernel, dim3((unsigned)((elems / 4 + 255) / 256), (unsigned)units), 256, 0, stream, r.seg_tot,
-               (const float*)r.seg_dec, r.s0, s.nseg, elems);
+    if ((e = go()) != cudaSuccess) return e;
+    e = launch(true, la_join_kernel, dim3((unsigned)((elems + 255) / 256), (unsigned)units), 256, 0, stream, r.seg_tot,
+               (const float*)r.seg_dec, r.s0, s.nseg, (int)elems);
     if (e != cudaSuccess) return e;
     dependent = true;
     s.totals = 0;
