@@ -58,7 +58,7 @@ struct GateSrc {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = 4 * lane + q;
-      x[q] = t < L ? gate(head_decay ? g[h] : g[(tok + t) * Hv + h]) : 0.f;
+      x[q] = t < L ? (head_decay ? g[h] : g[(tok + t) * Hv + h]) : 0.f;   // not touched here: still in flight
     }
   }
 };
@@ -71,11 +71,11 @@ __device__ __forceinline__ void add_pair(float& s, float& e, float ys, float ye)
 }
 
 __device__ __forceinline__ void scan_gates(const float (&x)[4], Gates& w, int lane) {
-  w.hi[0] = x[0];
+  w.hi[0] = gate(x[0]);
   w.lo[0] = 0.f;
 #pragma unroll
   for (int q = 1; q < 4; ++q) {
-    w.hi[q] = x[q];
+    w.hi[q] = gate(x[q]);
     w.lo[q] = 0.f;
     add_pair(w.hi[q], w.lo[q], w.hi[q - 1], w.lo[q - 1]);
   }

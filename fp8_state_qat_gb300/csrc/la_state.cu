@@ -26,9 +26,9 @@ namespace gdn {
 namespace la {
 namespace {
 
-constexpr int kWorkers = 512, kThreads = kWorkers + 96;
+constexpr int kThreads = 640;                // warps 0-7 state, 8-15 V's terms, 16 products, 17, 18 weights, 19 states out
 constexpr int kNV = 64;                      // value columns of a CTA
-constexpr int kHC = kNV / 4;                 // of a thread
+constexpr int kHC = kNV / 2;                 // of a thread of the state
 constexpr uint32_t kTmemCols = 128;          // two accumulators
 // shared memory: two K tiles, two V tiles, one or two sets of V's terms, the states on their way out, S
 constexpr uint32_t kOffV = 2 * kTile, kOffTerm = kOffV + 2 * kBlk, kTermSet = 3 * kBlk;
@@ -54,17 +54,18 @@ __host__ __device__ inline uint32_t off_other(const Params& p) { return off_out(
 inline uint32_t smem_bytes(const Params& p) { return off_other(p) + (p.other ? 2 * kBlk : 0) + 1024; }
 constexpr uint32_t kMaxSmem = kOffTerm + 2 * kTermSet + 2 * kBlk + 1024;
 
+constexpr int kW = 3;   // weights are computed up to three steps ahead
 struct Shared {
   uint64_t kfull[2], vfull[2];   // a step's tiles have landed
-  uint64_t wready[2], wfree[2];  // its weights are written; are read
+  uint64_t wready[kW], wfree[kW];   // its weights are written; are read
   uint64_t aready[2];            // its terms are written (and V is read)
-  uint64_t mma[2];               // its product is complete
+  uint64_t mma[2], accfree[2];   // its product is complete; is taken
   uint64_t sready, sfree;        // the state is laid out for its way out; has been read from there
   uint64_t ofull, oread;         // S of the step has landed; is read
   uint32_t tmem;
   int dead;
-  float decay[2], log_decay[2];  // Gam of a step; log Gam of the whole segment, in two parts
-  __align__(16) float w[2][kC];
+  float decay[kW], log_decay[2];   // Gam of a step; log Gam of the whole segment, in two parts
+  __align__(16) float w[kW][kC];
 };
 
 // 8 values -> three bf16 terms each
@@ -84,8 +85,9 @@ __device__ __forceinline__ void split3(const float2 (&x)[4], uint4& t1, uint4& t
   t3 = make_uint4(c[0], c[1], c[2], c[3]);
 }
 
-// Warps 0-15 weight V and hold the state; warp 16 loads and issues the products; warps 17 and 18 compute the
-// weights, of every other step each: the latency of a step's loads and sums is longer than the step.
+// Each group of warps walks the steps at its own pace: V's terms of a step are written while the products of
+// the step before run and the state takes those of the step before that. Two warps compute the weights, of
+// every other step each: the latency of a step's loads and sums is longer than the step.
 __global__ void __launch_bounds__(kThreads, 1)
 la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ CUtensorMap ty,
                 const __grid_constant__ CUtensorMap ts, const __grid_constant__ CUtensorMap to,
@@ -96,7 +98,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const uint32_t sbase = (raw + 1023u) & ~1023u;
   unsigned char* sm = smem_raw + (sbase - raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = warp & 3, part = warp >> 2;
+  const int quad = warp & 3, part = (warp >> 2) & 1;
   const uint32_t lane0 = 32u * quad;
   const int row = 32 * quad + lane;        // key channel
   const bool live = row < p.dk;            // dk 64: lanes 64-127 of the product are not used
@@ -126,15 +128,18 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(tc::smem_u32(&sh.kfull[i]), 1);
       tc::mbar_init(tc::smem_u32(&sh.vfull[i]), 1);
-      tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
-      tc::mbar_init(tc::smem_u32(&sh.wfree[i]), kWorkers / 32);
-      tc::mbar_init(tc::smem_u32(&sh.aready[i]), kWorkers / 32);
+      tc::mbar_init(tc::smem_u32(&sh.aready[i]), 8);
       tc::mbar_init(tc::smem_u32(&sh.mma[i]), 1);
+      tc::mbar_init(tc::smem_u32(&sh.accfree[i]), 8);
     }
-    tc::mbar_init(tc::smem_u32(&sh.sready), kWorkers / 32);
+    for (int i = 0; i < kW; ++i) {
+      tc::mbar_init(tc::smem_u32(&sh.wready[i]), 32);
+      tc::mbar_init(tc::smem_u32(&sh.wfree[i]), 16);
+    }
+    tc::mbar_init(tc::smem_u32(&sh.sready), 8);
     tc::mbar_init(tc::smem_u32(&sh.sfree), 1);
     tc::mbar_init(tc::smem_u32(&sh.ofull), 1);
-    tc::mbar_init(tc::smem_u32(&sh.oread), kWorkers / 32);
+    tc::mbar_init(tc::smem_u32(&sh.oread), 8);
     tc::mbar_fence_init();
     sh.dead = 0;
   }
@@ -152,10 +157,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * kNV + part * kHC;
   const int64_t seg_g = (((int64_t)unit * p.nseg + seg) * p.dk + row) * p.dv + vt * kNV + part * kHC;
 
-  if (warp == kWorkers / 32) {
-    // ---- loads and products ----
+  auto token = [&](int i) { return t0 + chunk_of(i) * kC; };
+  if (warp == 16) {
+    // ---- token tiles and products ----
     constexpr uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, kNV, true, true);
-    auto token = [&](int i) { return t0 + chunk_of(i) * kC; };
     auto load_k = [&](int i) {
       const uint32_t bar = tc::smem_u32(&sh.kfull[i & 1]), dst = sbase + (i & 1) * kTile;
       tc::mbar_expect_tx(bar, p.dk / 64 * kBlk);
@@ -166,29 +171,19 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       tc::mbar_expect_tx(bar, kBlk);
       tc::tma_load_3d(sbase + kOffV + (i & 1) * kBlk, &ty, bar, vt * kNV, h, token(i));
     };
-    auto state_row = [&](int i, int terms, int term) {   // of the stored states: this value tile's rows
-      const int item = (slot0 + chunk_of(i)) * Hv + h;
-      return ((item * terms + term) * tiles + vt) * p.dk;
-    };
-    auto load_other = [&](int i) {
-      tc::mbar_expect_tx(tc::smem_u32(&sh.ofull), 2 * p.dk * 128);
-      for (int t = 0; t < 2; ++t)
-        tc::tma_load_2d(sbase + off_other(p) + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
-    };
-    int ks = min(2, steps), vs = ks, os = p.other && steps ? 1 : 0, issued = 0;   // loads and products issued
-    if (lane == 0) {
+    int ks = min(2, steps), vs = ks, issued = 0;   // loads and products issued
+    if (lane == 0)
       for (int i = 0; i < vs; ++i) {
         load_v(i);
         load_k(i);
       }
-      if (os) load_other(0);
-    }
     __syncwarp();
     const uint32_t me = elect_one();
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const uint32_t turn = (i >> 1) & 1;
-      ok = wait(sh.dead, sh.aready[i & 1], turn) && wait(sh.dead, sh.kfull[i & 1], turn);
+      ok = wait(sh.dead, sh.accfree[i & 1], turn ^ 1) && wait(sh.dead, sh.kfull[i & 1], turn) &&
+           wait(sh.dead, sh.aready[i & 1], turn);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       const uint64_t ad = tc::make_sdesc(sbase + (i & 1) * kTile, kBlk, 1024);
@@ -200,53 +195,71 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           mma_bf16_w(tmem + (i & 1) * kNV, dadv(ad, k * 2048), dadv(bd, t * kBlk + k * 2048), idesc, t + k > 0, me);
       mma_commit_w(tc::smem_u32(&sh.mma[i & 1]), me);
       issued = i + 1;
-      if (i + 2 < steps) {   // V of this step is weighted
+      if (i + 2 < steps) {   // V of this step is weighted; K is free when its product is complete
         if (lane == 0) load_v(i + 2);
         ++vs;
-      }
-      if (p.store) {
-        ok = wait(sh.dead, sh.sready, i & 1);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (lane == 0) {
-          for (int t = 0; t < p.terms; ++t)
-            tc::tma_store_2d(&ts, sbase + off_out(p) + t * kBlk, 0, state_row(i, p.terms, t));
-          tc::bulk_commit();
-        }
-        __syncwarp();
-      }
-      if (p.other && i + 1 < steps) {
-        ok = wait(sh.dead, sh.oread, i & 1);
-        if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (lane == 0) load_other(i + 1);
-        ++os;
-      }
-      if (i + 2 < steps) {   // K of this step is free when its product is complete
         ok = wait(sh.dead, sh.mma[i & 1], turn);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (lane == 0) load_k(i + 2);
         ++ks;
-      }
-      if (p.store && lane == 0) {
-        tc::bulk_wait_read();
-        tc::mbar_arrive(tc::smem_u32(&sh.sfree));
       }
       __syncwarp();
     }
     if (lane == 0 && !ok) {   // nothing of this CTA is in flight when it ends
       for (int i = max(0, ks - 2); i < ks; ++i) tc::mbar_wait(tc::smem_u32(&sh.kfull[i & 1]), (i >> 1) & 1, 1u << 22);
       for (int i = max(0, vs - 2); i < vs; ++i) tc::mbar_wait(tc::smem_u32(&sh.vfull[i & 1]), (i >> 1) & 1, 1u << 22);
-      if (os) tc::mbar_wait(tc::smem_u32(&sh.ofull), (os - 1) & 1, 1u << 22);
       if (issued) tc::mbar_wait(tc::smem_u32(&sh.mma[(issued - 1) & 1]), ((issued - 1) >> 1) & 1, 1u << 22);
+    }
+  } else if (warp == 19) {
+    // ---- states out, S in ----
+    auto state_row = [&](int i, int terms, int term) {   // of the stored states: this value tile's rows
+      const int item = (slot0 + chunk_of(i)) * Hv + h;
+      return ((item * terms + term) * tiles + vt) * p.dk;
+    };
+    auto load_other = [&](int i) {
+      tc::mbar_expect_tx(tc::smem_u32(&sh.ofull), 2 * p.dk * 128);
+      for (int t = 0; t < 2; ++t)
+        tc::tma_load_2d(sbase + off_other(p) + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
+    };
+    int os = 0;
+    if (p.other && steps) {
+      if (lane == 0) load_other(0);
+      os = 1;
+    }
+#pragma unroll 1
+    for (int i = 0; i < steps && p.store; ++i) {
+      ok = wait(sh.dead, sh.sready, i & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (lane == 0) {
+        for (int t = 0; t < p.terms; ++t)
+          tc::tma_store_2d(&ts, sbase + off_out(p) + t * kBlk, 0, state_row(i, p.terms, t));
+        tc::bulk_commit();
+      }
+      __syncwarp();
+      if (p.other && i + 1 < steps) {
+        ok = wait(sh.dead, sh.oread, i & 1);
+        if (!(ok = __all_sync(0xffffffffu, ok))) break;
+        if (lane == 0) load_other(i + 1);
+        ++os;
+      }
+      if (lane == 0) {
+        tc::bulk_wait_read();
+        tc::mbar_arrive(tc::smem_u32(&sh.sfree));
+      }
+      __syncwarp();
+    }
+    if (lane == 0 && !ok) {
+      if (os) tc::mbar_wait(tc::smem_u32(&sh.ofull), (os - 1) & 1, 1u << 22);
       tc::bulk_wait_read();
     }
-  } else if (warp > kWorkers / 32) {
+  } else if (warp > 16) {
     // ---- weights ----
-    const int which = warp - kWorkers / 32 - 1;
+    const int which = warp - 17;
     float gx[4], log_decay = 0.f;   // of this warp's steps
     auto gates = [&](int i) { p.gates.load(gx, t0 + (int64_t)chunk_of(i) * kC, h, rows_of(chunk_of(i)), lane); };
     if (which < steps) gates(which);
     for (int i = which; i < steps; i += 2) {
-      ok = wait(sh.dead, sh.wfree[i & 1], ((i >> 1) & 1) ^ 1);
+      ok = wait(sh.dead, sh.wfree[i % kW], ((i / kW) & 1) ^ 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       const int L = rows_of(chunk_of(i));
       Gates w;
@@ -258,12 +271,50 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         v[q] = 4 * lane + q < L ? p.scale * expf((p.reverse ? w.pre(q) : w.after(q)) + far) : 0.f;
-      *reinterpret_cast<float4*>(&sh.w[i & 1][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-      if (lane == 0) sh.decay[i & 1] = expf(all);
+      *reinterpret_cast<float4*>(&sh.w[i % kW][4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+      if (lane == 0) sh.decay[i % kW] = expf(all);
       log_decay += all;
-      tc::mbar_arrive(tc::smem_u32(&sh.wready[i & 1]));
+      tc::mbar_arrive(tc::smem_u32(&sh.wready[i % kW]));
     }
     if (lane == 0) sh.log_decay[which] = log_decay;
+  } else if (warp >= 8) {
+    // ---- V's terms: this thread's 16-byte pieces, rows r, r + 32, .. of piece tid % 8 ----
+    const int vrow = (tid - 256) >> 3;
+    const uint32_t voff = tc::sw128(vrow, (tid & 7) * 16);
+#pragma unroll 1
+    for (int i = 0; i < steps; ++i) {
+      const int L = rows_of(chunk_of(i));
+      ok = wait(sh.dead, sh.vfull[i & 1], (i >> 1) & 1) && wait(sh.dead, sh.wready[i % kW], (i / kW) & 1);
+      // the products that read this set of terms before are complete
+      if (i >= p.sets) ok = ok && wait(sh.dead, sh.mma[(i - p.sets) & 1], ((i - p.sets) >> 1) & 1);
+      const unsigned char* v = sm + kOffV + (i & 1) * kBlk + voff;
+      unsigned char* t = sm + kOffTerm + (p.sets == 2 ? (i & 1) * kTermSet : 0) + voff;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float w = sh.w[i % kW][vrow + 32 * e];
+        uint4 q = *reinterpret_cast<const uint4*>(v + 4096 * e);
+        if (vrow + 32 * e >= L) q = make_uint4(0, 0, 0, 0);   // another sequence's
+        const float2 w2 = make_float2(w, w);
+        const float2 x[4] = {__fmul2_rn(unpack_bf16(q.x), w2), __fmul2_rn(unpack_bf16(q.y), w2),
+                             __fmul2_rn(unpack_bf16(q.z), w2), __fmul2_rn(unpack_bf16(q.w), w2)};
+        uint4 t1, t2, t3;
+        split3(x, t1, t2, t3);
+        *reinterpret_cast<uint4*>(t + 4096 * e) = t1;
+        *reinterpret_cast<uint4*>(t + 4096 * e + kBlk) = t2;
+        *reinterpret_cast<uint4*>(t + 4096 * e + 2 * kBlk) = t3;
+      }
+      if (L < kC) {   // uniform: K's tail rows would meet zero weights, but not with a NaN
+        ok = ok && wait(sh.dead, sh.kfull[i & 1], (i >> 1) & 1);
+        zero_tail_rows(sm + (i & 1) * kTile, p.dk / 64, tid - 256, L);
+      }
+      tc::fence_proxy_async_smem();
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(tc::smem_u32(&sh.wfree[i % kW]));
+        tc::mbar_arrive(tc::smem_u32(&sh.aready[i & 1]));
+      }
+    }
   } else {
     // ---- the state ----
     const float* src = p.totals ? nullptr : p.nseg > 1 ? p.seg_tot + seg_g : p.s0 ? p.s0 + sbase_g : nullptr;
@@ -272,66 +323,11 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       const float4 v = src && live ? *reinterpret_cast<const float4*>(src + j) : make_float4(0.f, 0.f, 0.f, 0.f);
       s[j] = v.x; s[j + 1] = v.y; s[j + 2] = v.z; s[j + 3] = v.w;
     }
-    const bool work = 32 * quad < p.dk;   // uniform in the warp
-    float decay = 1.f;                    // Gam of the chunk whose product is in flight
-    auto take = [&](int i) {              // the product of step i -> the state
-      ok = ok && wait(sh.dead, sh.mma[i & 1], (i >> 1) & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      tc::tc_fence_after();
-      if (!work) return;
-      float v[kHC];
-      tc::tmem_ld16(tc::tmem_addr(tmem, lane0, (i & 1) * kNV + part * kHC), v);
-      tc::tmem_ld_wait();
-      const float2 d2 = make_float2(decay, decay);
-#pragma unroll
-      for (int j = 0; j < kHC; j += 2) {
-        const float2 r = __ffma2_rn(d2, make_float2(s[j], s[j + 1]), make_float2(v[j], v[j + 1]));
-        s[j] = r.x;
-        s[j + 1] = r.y;
-      }
-    };
-    // this thread's 16-byte pieces of V and its terms: rows tid / 8 and 64 more, piece tid % 8
-    const int vrow = tid >> 3;
-    const uint32_t voff = tc::sw128(vrow, (tid & 7) * 16);
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
-      const int c = chunk_of(i), L = rows_of(c);
-      if (p.sets == 1 && i > 0) take(i - 1);   // its terms give way
-      ok = ok && wait(sh.dead, sh.vfull[i & 1], (i >> 1) & 1) && wait(sh.dead, sh.wready[i & 1], (i >> 1) & 1);
-      const float decay_i = sh.decay[i & 1];
-      {
-        const unsigned char* v = sm + kOffV + (i & 1) * kBlk + voff;
-        unsigned char* t = sm + kOffTerm + (p.sets == 2 ? (i & 1) * kTermSet : 0) + voff;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float w = sh.w[i & 1][vrow + 64 * e];
-          uint4 q = *reinterpret_cast<const uint4*>(v + 8192 * e);
-          if (vrow + 64 * e >= L) q = make_uint4(0, 0, 0, 0);   // another sequence's
-          const float2 w2 = make_float2(w, w);
-          const float2 x[4] = {__fmul2_rn(unpack_bf16(q.x), w2), __fmul2_rn(unpack_bf16(q.y), w2),
-                               __fmul2_rn(unpack_bf16(q.z), w2), __fmul2_rn(unpack_bf16(q.w), w2)};
-          uint4 t1, t2, t3;
-          split3(x, t1, t2, t3);
-          *reinterpret_cast<uint4*>(t + 8192 * e) = t1;
-          *reinterpret_cast<uint4*>(t + 8192 * e + kBlk) = t2;
-          *reinterpret_cast<uint4*>(t + 8192 * e + 2 * kBlk) = t3;
-        }
-      }
-      if (L < kC) {   // uniform: K's tail rows would meet zero weights, but not with a NaN
-        ok = ok && wait(sh.dead, sh.kfull[i & 1], (i >> 1) & 1);
-        zero_tail_rows(sm + (i & 1) * kTile, p.dk / 64, tid, L);
-      }
-      tc::fence_proxy_async_smem();
-      if (!(ok = __all_sync(0xffffffffu, ok))) break;
-      tc::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        tc::mbar_arrive(tc::smem_u32(&sh.wfree[i & 1]));
-        tc::mbar_arrive(tc::smem_u32(&sh.aready[i & 1]));
-      }
-      if (p.sets == 2 && i > 0) take(i - 1);
+      const int c = chunk_of(i);
       if (p.store) {   // the state before this chunk, as 128-byte swizzled rows of 64 columns
-        if (i > 0) ok = ok && wait(sh.dead, sh.sfree, (i - 1) & 1);
+        if (i > 0) ok = wait(sh.dead, sh.sfree, (i - 1) & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
         if (live) {
 #pragma unroll
@@ -351,10 +347,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.sready));
       }
+      float2 x = make_float2(0.f, 0.f);
       if (p.other) {
-        ok = ok && wait(sh.dead, sh.ofull, i & 1);
+        ok = wait(sh.dead, sh.ofull, i & 1);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        float2 x = make_float2(0.f, 0.f);
         if (live) {
 #pragma unroll
           for (int j = 0; j < kHC; j += 8) {
@@ -369,13 +365,34 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
         }
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(tc::smem_u32(&sh.oread));
-        const float sum = warp_sum(x.x + x.y);
-        if (lane == 0)
-          p.edge[(((int64_t)(slot0 + c) * Hv + h) * tiles + vt) * (kWorkers / 32) + warp] = decay_i * sum;
       }
-      decay = decay_i;
+      ok = wait(sh.dead, sh.wready[i % kW], (i / kW) & 1);
+      const float decay = sh.decay[i % kW];
+      if (p.other) {
+        const float sum = warp_sum(x.x + x.y);
+        if (lane == 0) p.edge[(((int64_t)(slot0 + c) * Hv + h) * tiles + vt) * 8 + warp] = decay * sum;
+      }
+      ok = ok && wait(sh.dead, sh.mma[i & 1], (i >> 1) & 1);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      tc::tc_fence_after();
+      if (32 * quad < p.dk) {   // uniform in the warp
+        float v[kHC];
+        ld32(tmem, lane0, (i & 1) * kNV + part * kHC, v);
+        const float2 d2 = make_float2(decay, decay);
+#pragma unroll
+        for (int j = 0; j < kHC; j += 2) {
+          const float2 r = __ffma2_rn(d2, make_float2(s[j], s[j + 1]), make_float2(v[j], v[j + 1]));
+          s[j] = r.x;
+          s[j + 1] = r.y;
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(tc::smem_u32(&sh.wfree[i % kW]));
+        tc::mbar_arrive(tc::smem_u32(&sh.accfree[i & 1]));
+      }
     }
-    if (ok && steps) take(steps - 1);
   }
   if (!ok) {
     *(volatile int*)&sh.dead = 1;
@@ -387,9 +404,8 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
   if (sh.dead) return;
-  if (warp >= kWorkers / 32) {
-    if (p.totals && tid == kWorkers && vt == 0)
-      p.seg_dec[unit * p.nseg + seg] = expf(sh.log_decay[0] + sh.log_decay[1]);
+  if (warp >= 8) {
+    if (p.totals && tid == 256 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(sh.log_decay[0] + sh.log_decay[1]);
     return;
   }
   float* dst = p.totals ? p.seg_tot + seg_g : p.sT && seg == p.nseg - 1 ? p.sT + sbase_g : nullptr;
@@ -446,7 +462,7 @@ int state_segments(const LaProblem& p) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(kSMs / walks, chunks / 4));
 }
 
-int edge_parts(const LaProblem& p) { return p.dv / kNV * (kWorkers / 32); }
+int edge_parts(const LaProblem& p) { return p.dv / kNV * 8; }
 
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream) {
   const int64_t units = (int64_t)p.N * p.Hv, tokens = (int64_t)p.B * p.T;
