@@ -126,6 +126,21 @@ __device__ __forceinline__ void mma_commit_w(uint32_t mbar, uint32_t me) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(mbar), "r"(me)
       : "memory");
 }
+// copies likewise
+__device__ __forceinline__ void mbar_expect_w(uint32_t addr, uint32_t bytes, uint32_t me) {
+  asm volatile(
+      "{ .reg .pred q; .reg .b64 st; setp.ne.b32 q, %2, 0; @q mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1; }" ::"r"(addr),
+      "r"(bytes), "r"(me)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_w(uint32_t dst, const CUtensorMap* map, uint32_t mbar, int c0, int c1, int c2,
+                                              uint32_t me) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.b32 q, %6, 0; @q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4, %5}], [%2]; }" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar), "r"(c0), "r"(c1), "r"(c2), "r"(me)
+      : "memory");
+}
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t me;
   asm volatile("{ .reg .pred q; elect.sync _|q, 0xffffffff; selp.u32 %0, 1, 0, q; }" : "=r"(me));

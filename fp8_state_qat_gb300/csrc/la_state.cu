@@ -161,29 +161,37 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   if (warp == 16) {
     // ---- token tiles and products ----
     constexpr uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, kNV, true, true);
+    const uint32_t me = elect_one();
+    const bool two = p.dk == 128;
+    const uint32_t kbytes = two ? kTile : kBlk;
     auto load_k = [&](int i) {
       const uint32_t bar = tc::smem_u32(&sh.kfull[i & 1]), dst = sbase + (i & 1) * kTile;
-      tc::mbar_expect_tx(bar, p.dk / 64 * kBlk);
-      for (int b = 0; b < p.dk / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &tx, bar, 64 * b, hq, token(i));
+      const int tok = token(i);
+      mbar_expect_w(bar, kbytes, me);
+      tma_load_3d_w(dst, &tx, bar, 0, hq, tok, me);
+      if (two) tma_load_3d_w(dst + kBlk, &tx, bar, 64, hq, tok, me);
     };
     auto load_v = [&](int i) {
       const uint32_t bar = tc::smem_u32(&sh.vfull[i & 1]);
-      tc::mbar_expect_tx(bar, kBlk);
-      tc::tma_load_3d(sbase + kOffV + (i & 1) * kBlk, &ty, bar, vt * kNV, h, token(i));
+      mbar_expect_w(bar, kBlk, me);
+      tma_load_3d_w(sbase + kOffV + (i & 1) * kBlk, &ty, bar, vt * kNV, h, token(i), me);
     };
-    int ks = min(2, steps), vs = ks, issued = 0;   // loads and products issued
-    if (lane == 0)
-      for (int i = 0; i < vs; ++i) {
-        load_v(i);
-        load_k(i);
-      }
-    __syncwarp();
-    const uint32_t me = elect_one();
+    const int ks0 = min(2, steps);
+    int ks = ks0, vs = ks0, issued = 0;   // loads and products issued
+    for (int i = 0; i < ks0; ++i) {
+      load_v(i);
+      load_k(i);
+    }
 #pragma unroll 1
     for (int i = 0; i < steps; ++i) {
       const uint32_t turn = (i >> 1) & 1;
-      ok = wait(sh.dead, sh.accfree[i & 1], turn ^ 1) && wait(sh.dead, sh.kfull[i & 1], turn) &&
-           wait(sh.dead, sh.aready[i & 1], turn);
+      ok = wait(sh.dead, sh.aready[i & 1], turn);
+      if (!(ok = __all_sync(0xffffffffu, ok))) break;
+      if (i + 2 < steps) {   // V of this step is weighted
+        load_v(i + 2);
+        ++vs;
+      }
+      ok = wait(sh.dead, sh.accfree[i & 1], turn ^ 1) && wait(sh.dead, sh.kfull[i & 1], turn);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       tc::tc_fence_after();
       const uint64_t ad = tc::make_sdesc(sbase + (i & 1) * kTile, kBlk, 1024);
@@ -195,15 +203,12 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
           mma_bf16_w(tmem + (i & 1) * kNV, dadv(ad, k * 2048), dadv(bd, t * kBlk + k * 2048), idesc, t + k > 0, me);
       mma_commit_w(tc::smem_u32(&sh.mma[i & 1]), me);
       issued = i + 1;
-      if (i + 2 < steps) {   // V of this step is weighted; K is free when its product is complete
-        if (lane == 0) load_v(i + 2);
-        ++vs;
+      if (i + 2 < steps) {   // K is free when its product is complete
         ok = wait(sh.dead, sh.mma[i & 1], turn);
         if (!(ok = __all_sync(0xffffffffu, ok))) break;
-        if (lane == 0) load_k(i + 2);
+        load_k(i + 2);
         ++ks;
       }
-      __syncwarp();
     }
     if (lane == 0 && !ok) {   // nothing of this CTA is in flight when it ends
       for (int i = max(0, ks - 2); i < ks; ++i) tc::mbar_wait(tc::smem_u32(&sh.kfull[i & 1]), (i >> 1) & 1, 1u << 22);
