@@ -1,4 +1,5 @@
-"""Compile the CUDA library ``libgdnqat.so`` in-tree for sm_103a.
+"""Compile the CUDA library ``libgdnqat.so`` in-tree for sm_103a, and the Python extension
+``gdnqat_layer.so`` (csrc/layer_ext.cpp, g++ against torch's headers) beside it.
 
 Each ``csrc/*.cu`` is compiled to an object in parallel (one ``-gencode``, no cmake), then
 linked into ``fp8_state_qat_gb300/_lib/libgdnqat.so`` with the CUDA runtime linked
@@ -18,6 +19,8 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ_DIR = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libgdnqat.so")
+EXT_SOURCE = os.path.join(CSRC, "layer_ext.cpp")
+EXT_PATH = os.path.join(LIB_DIR, "gdnqat_layer.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,8 +52,34 @@ def newer_than(out: str, deps) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def _ext_deps():
+    return [EXT_SOURCE, os.path.join(ROOT, "include", "gdnqat.h"), __file__]
+
+
 def up_to_date() -> bool:
-    return newer_than(LIB_PATH, _deps())
+    return newer_than(LIB_PATH, _deps()) and newer_than(EXT_PATH, _ext_deps())
+
+
+def compile_extension(out: str = EXT_PATH) -> str:
+    """g++ the argument checks and allocations of layer.py against this Python and this torch."""
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    os.makedirs(os.path.dirname(out), exist_ok=True)
+    tmp = out + f".tmp{os.getpid()}"
+    include = [os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               os.path.join(cuda, "include")]
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden", *[f"-isystem{d}" for d in include],
+           "-I", sysconfig.get_paths()["include"], EXT_SOURCE, "-o", tmp, "-L" + os.path.join(home, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + os.path.join(cuda, "lib64"), "-lcudart"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {os.path.basename(EXT_SOURCE)}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, out)
+    return out
 
 
 def compile_library(sources, out: str, obj_dir: str, verbose: bool = False) -> str:
@@ -88,10 +117,17 @@ def compile_library(sources, out: str, obj_dir: str, verbose: bool = False) -> s
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu into libgdnqat.so (skipped when it is up to date)."""
-    if not force and up_to_date():
-        return LIB_PATH
-    return compile_library(_sources(), LIB_PATH, OBJ_DIR, verbose=verbose)
+    """Compile csrc/*.cu into libgdnqat.so and csrc/layer_ext.cpp into gdnqat_layer.so, side by side (each
+    skipped when it is up to date)."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        ext = None
+        if force or not newer_than(EXT_PATH, _ext_deps()):
+            ext = ex.submit(compile_extension)
+        if force or not newer_than(LIB_PATH, _deps()):
+            compile_library(_sources(), LIB_PATH, OBJ_DIR, verbose=verbose)
+        if ext is not None:
+            ext.result()
+    return LIB_PATH
 
 
 if __name__ == "__main__":
