@@ -87,6 +87,7 @@ __device__ __forceinline__ void load_w(const void* w, int w_bf16, int D, int t, 
   else load_row<TPR, VEC>(static_cast<const float*>(w), D, t, v);
 }
 
+constexpr int kSums = 7;               // values that one reduction sums at most
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 // Resident CTAs an SM that a backward's registers leave room for (and its launch asks for): its rows in flight
 // need about 100 registers a thread.
@@ -97,13 +98,13 @@ constexpr int bwd_per_sm(int tpr) { return tpr <= 256 ? 2 : 1; }
 template <int TPR, int M>
 struct RowSum {
   static constexpr int kWarps = threads_of(TPR) / 32;
-  static __device__ __forceinline__ void run(float (&v)[M], float (*smem)[kWarps][2], int& slot) {
+  static __device__ __forceinline__ void run(float (&v)[M], float (*smem)[kWarps][kSums], int& slot) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
     for (int m = 0; m < M; ++m)
 #pragma unroll
       for (int o = W / 2; o > 0; o >>= 1) v[m] += __shfl_xor_sync(0xffffffffu, v[m], o);
-    if (TPR > 32) {
+    if constexpr (TPR > 32) {
       const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
       if (lane == 0)
 #pragma unroll
@@ -132,7 +133,7 @@ __global__ void __launch_bounds__(threads_of(TPR))
 gated_norm_fwd_kernel(const X* __restrict__ x, const __nv_bfloat16* __restrict__ z, const void* __restrict__ w,
                       int w_bf16, __nv_bfloat16* __restrict__ y, int64_t rows, int D, float eps) {
   constexpr int RPC = threads_of(TPR) / TPR;
-  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float sm[2][threads_of(TPR) / 32][kSums];
   int slot = 0;
   const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
   float wv[E];
@@ -196,7 +197,7 @@ gated_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dy, const X* __restrict_
                       X* __restrict__ dx, __nv_bfloat16* __restrict__ dz, float* __restrict__ part, int64_t rows,
                       int D, float eps) {
   constexpr int RPC = threads_of(TPR) / TPR;
-  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float sm[2][threads_of(TPR) / 32][kSums];
   __shared__ float red[RPC > 1 ? threads_of(TPR) * E : 1];
   int slot = 0;
   const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
@@ -252,7 +253,7 @@ residual_norm_fwd_kernel(const __nv_bfloat16* __restrict__ y, const H* h, const 
                          const void* __restrict__ w_pre, int w_bf16, H* h_out,
                          __nv_bfloat16* __restrict__ x, int64_t rows, int D, float alpha, float eps) {
   constexpr int RPC = threads_of(TPR) / TPR;
-  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float sm[2][threads_of(TPR) / 32][kSums];
   int slot = 0;
   const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
   float w1[E], w2[E];
@@ -308,7 +309,7 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
                          H* dh, float* __restrict__ part_pre, float* __restrict__ part_post, int64_t rows,
                          int D, float alpha, float eps) {
   constexpr int RPC = threads_of(TPR) / TPR;
-  __shared__ float sm[2][threads_of(TPR) / 32][2];
+  __shared__ float sm[2][threads_of(TPR) / 32][kSums];
   __shared__ float red[RPC > 1 ? threads_of(TPR) * E : 1];
   int slot = 0;
   const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
@@ -336,34 +337,81 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
     nd.get(dv);
     ndh.get(dhv);
     load(r + stride);
-    float ry = 1.f;
-    if (POST) {
-      float s[1] = {0.f};
+    // With u = y w_post, p = dx w_pre, a = alpha r_y, h' = h + a u, all sums of the row are polynomials in a of
+    // seven sums that need no other first: one reduction instead of three in a row.
+    constexpr bool ONE = POST && (TPR <= 32 || TPR >= 256);
+    float ry = 1.f, ss, sp, su = 0.f, gu = 0.f, pu = 0.f;   // sums of h' h', p h', h' u, dh' u, p u
+    if (ONE) {
+      float s[7] = {};
 #pragma unroll
-      for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
-      RowSum<TPR, 1>::run(s, sm, slot);
+      for (int e = 0; e < E; ++e) {
+        const float u = yv[e] * w2[e], q = dv[e] * w1[e];
+        s[0] = fmaf(yv[e], yv[e], s[0]);
+        s[1] = fmaf(hv[e], hv[e], s[1]);
+        s[2] = fmaf(hv[e], u, s[2]);
+        s[3] = fmaf(u, u, s[3]);
+        s[4] = fmaf(q, hv[e], s[4]);
+        s[5] = fmaf(q, u, s[5]);
+        s[6] = fmaf(dhv[e], u, s[6]);
+      }
+      RowSum<TPR, 7>::run(s, sm, slot);
       ry = rsqrtf(fmaf(s[0], inv_d, eps));
-    }
-    float s[2] = {0.f, 0.f};
+      const float a = alpha * ry;
+      ss = fmaf(a, fmaf(a, s[3], 2.f * s[2]), s[1]);
+      sp = fmaf(a, s[5], s[4]);
+      su = fmaf(a, s[3], s[2]);
+      gu = s[6];
+      pu = s[5];
+      // where h and a u nearly cancel, h' h' is summed from h' itself: decided alike by all who share a reduction
+      bool small = !(ss >= 0.1f * fmaf(a * a, s[3], s[1])) && live;
+      if (TPR <= 32) small = __any_sync(0xffffffffu, small);
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-      hv[e] = fmaf(alpha, POST ? yv[e] * ry * w2[e] : yv[e], hv[e]);
-      s[0] = fmaf(hv[e], hv[e], s[0]);
-      s[1] = fmaf(dv[e] * w1[e], hv[e], s[1]);
+      for (int e = 0; e < E; ++e) hv[e] = fmaf(a, yv[e] * w2[e], hv[e]);
+      if (small) {
+        float x[3] = {};
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[0] = fmaf(hv[e], hv[e], x[0]);
+          x[1] = fmaf(dv[e] * w1[e], hv[e], x[1]);
+          x[2] = fmaf(hv[e], yv[e] * w2[e], x[2]);
+        }
+        RowSum<TPR, 3>::run(x, sm, slot);
+        ss = x[0];
+        sp = x[1];
+        su = x[2];
+      }
+    } else {
+      if (POST) {
+        float s[1] = {0.f};
+#pragma unroll
+        for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
+        RowSum<TPR, 1>::run(s, sm, slot);
+        ry = rsqrtf(fmaf(s[0], inv_d, eps));
+      }
+      float s[2] = {0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        hv[e] = fmaf(alpha, POST ? yv[e] * ry * w2[e] : yv[e], hv[e]);
+        s[0] = fmaf(hv[e], hv[e], s[0]);
+        s[1] = fmaf(dv[e] * w1[e], hv[e], s[1]);
+      }
+      RowSum<TPR, 2>::run(s, sm, slot);
+      ss = s[0];
+      sp = s[1];
     }
-    RowSum<TPR, 2>::run(s, sm, slot);
-    const float rh = rsqrtf(fmaf(s[0], inv_d, eps));
-    const float c = s[1] * inv_d * rh * rh;
+    const float rh = rsqrtf(fmaf(ss, inv_d, eps));
+    const float c = sp * inv_d * rh * rh;
     float q[1] = {0.f};
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       acc[0][e] = fmaf(dv[e], hv[e] * rh, acc[0][e]);
       dhv[e] += rh * fmaf(-c, hv[e], dv[e] * w1[e]);
-      if (POST) q[0] = fmaf(alpha * dhv[e] * w2[e], yv[e], q[0]);
+      if (POST && !ONE) q[0] = fmaf(alpha * dhv[e] * w2[e], yv[e], q[0]);
     }
+    if (ONE) q[0] = alpha * (gu + rh * (pu - c * su));
     if (live) store_row<TPR, VEC>(dh + r * D, D, t, dhv);
     if (POST) {
-      RowSum<TPR, 1>::run(q, sm, slot);
+      if (!ONE) RowSum<TPR, 1>::run(q, sm, slot);
       const float cy = q[0] * inv_d * ry * ry;
 #pragma unroll
       for (int e = 0; e < E; ++e) {

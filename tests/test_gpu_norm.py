@@ -66,6 +66,28 @@ def test_residual_norm(gdn, R, D, th, tw, post):
         near(d2, want[5], TOL_W)
 
 
+@pytest.mark.parametrize("D", [64, 200, 256, 300, 1000, 2048, 8192])
+def test_stream_that_cancels(gdn, D):
+    """Rows whose h nearly cancels alpha n, beside ordinary ones: the sums over h_out keep their accuracy."""
+    R = 21
+    y, dx, dh = rows_of(R, D, BF, 1), rows_of(R, D, BF, 2), rows_of(R, D, F32, 3)
+    w1, w2 = (1 + 0.3 * rows_of(1, D, F32, s)[0] for s in (4, 5))
+    n = ref.residual_norm(y, torch.zeros(R, D), w1, w2, 0.5, 1e-6)[0]
+    h = rows_of(R, D, F32, 6)
+    for r, keep in ((3, 1e-3), (4, 0.0), (11, 0.2), (20, 0.05)):
+        h[r] = (-n[r] * (1 - keep)).float() + (0 if keep else 1e-2 * h[r])
+    want = ref.residual_norm(y, h, w1, w2, 0.5, 1e-6, dx, dh)
+    c = [t.cuda() for t in (y, h, w1, w2)]
+    got = gdn.residual_norm_fwd(*c, alpha=0.5) + gdn.residual_norm_bwd(dx.cuda(), dh.cuda(), *c, alpha=0.5)
+    # h_out of those rows has lost up to 10 bits of h to the cancellation itself: 2^-24 x 1000 = 6e-5 of it; it is of
+    # the size of the others' rounding there, but the gradients divide by it, so they are held row by row
+    for a, b in zip(got[1:4], want[1:4]):
+        for r in range(R):
+            e = ref.rel(a[r], b[r])
+            assert e <= TOL[a.dtype] + (1e-3 if r in (3, 4) else 2e-5 if r in (11, 20) else 0), (r, e)
+    near(got[0], want[0])
+
+
 def test_many_rows(gdn):
     """More rows than the grid takes at once."""
     R, D = 40000, 64
