@@ -17,11 +17,16 @@
 // Roundings to bf16: the weighted scores and the state, each once, against outputs that are bf16
 // themselves; everything else is fp32.
 //
-// What bounds it is the traffic: 3 or 4 token tiles and 1 or 2 state terms in (32 KB each at d = 128), one tile
-// out, for about 1 us of tensor-core and exponential work. So one persistent CTA per SM keeps a ring of
-// six 32 KB tiles filled ahead by one TMA thread, across items; one thread issues the products; four warps
-// weight the scores; four others write the outputs of the same item while the first go on to
-// the next. The roles of one chunk run next to each other and read the same tiles from L2.
+// What bounds it is the traffic: 3 or 4 token tiles and 1 to 4 state terms in (32 KB each at d = 128), one tile out a
+// role. So one persistent CTA per SM keeps six 32 KB tiles filled ahead by TMA, across items; the three roles of a
+// chunk follow each other on the same token tiles; one warp issues the products; one computes the decays an
+// item ahead; eight weight the scores; four write the outputs of an item while the others go on to the next. The
+// loop bodies are kept small and shared by all roles: unrolled per block and role, the code outgrew the instruction cache
+// and the same work took 4 (o) to 10 times (gradients) as long.
+//
+// At 4 x 4096 tokens, 16 heads, d 128: o 55 us, 338 MB of tiles, 6.2 TB/s (0.92 of the measured copy bandwidth); dq, dk, dv
+// 162 us, 743 MB, 4.6 TB/s: all four token tiles of a chunk are in use until its last role, and the next chunk's
+// arrive 3 us after they fall free.
 #include <algorithm>
 #include <cstddef>
 

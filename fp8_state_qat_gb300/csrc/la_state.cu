@@ -10,13 +10,17 @@
 // K stays as TMA left it (MN-major A operand). The weights go to the V side: w_i v_i (fp32) is written as
 // three bf16 terms (24 bits, so the state has fp32 accuracy; two terms leave 2^-17 of it), in V's own
 // swizzled places, so that a thread moves 16 bytes at a time and nothing is transposed. (Weighting K instead,
-// through tensor memory, takes a 16-bit load an element and twice the elements: 64 us against the figures below.)
+// through tensor memory, takes a 16-bit load an element and twice the elements: 64 us against 56.)
 // The terms of chunk c + 1 are written while the products of chunk c run.
 // Tail rows of a partial chunk belong to another sequence, so they are zeroed, not just weighted by zero.
 //
 // Few sequences and heads: each walk is cut into segments, a first launch computes every segment's
 // contribution from a zero state, a scan joins them, and the second launch walks all segments at once
 // from their true starting states.
+//
+// At 4 x 4096 tokens, 16 heads, d 128 (128 CTAs of 32 steps): forwards 48 us, backwards 53 us (two-term S) and 74 us
+// (dS, with S read again for <S, dS>). Bound by tile traffic: 48 KB in and 16 to 64 KB out or in again a step, K by both
+// value tiles' CTAs, 5.6 to 6.5 TB/s from L2; a step takes 2.4 k cycles, its products 1.0 k, its conversion 1.4 k.
 #include <algorithm>
 
 #include "la_chunk.cuh"
@@ -453,18 +457,21 @@ constexpr int kSMs = 152;
 
 int64_t la_slots(const LaProblem& p) { return (int64_t)p.B * p.T / kC + p.N; }
 
-// One CTA of a walk runs per SM. Splitting walks costs a second pass over K and V, so it is done only
-// when half of the SMs or fewer have one, and then a segment keeps at least 4 chunks.
+// One CTA of a walk runs per SM, and a split walk takes two passes over K and V and a join. Forward at one
+// sequence, d 128, whole walks against split ones: T 16384, 16 walks, 9 segments 190 -> 82 us; 50 walks, 3
+// segments 243 -> 207 us; 60 walks, 2 segments 260 -> 267 us; T 4096, 8 walks, 8 segments 52 -> 34 us; 50
+// walks, 3 segments 69 -> 69 us; T 1024, 2 segments 25 -> 32 us. So a walk is split into three segments or more
+// or not at all, and a segment keeps at least 4 chunks.
 int state_segments(const LaProblem& p) {
-  const int64_t walks = (int64_t)p.N * p.Hv * (p.dv / 64);
-  if (walks == 0 || walks > kSMs / 2) return 1;
+  const int64_t walks = (int64_t)p.N * p.Hv * (p.dv / kNV);
+  if (walks == 0 || walks > kSMs / 3) return 1;
   int64_t longest = p.T;
   if (p.cu_host) {
     longest = 0;
     for (int n = 0; n < p.N; ++n) longest = std::max<int64_t>(longest, p.cu_host[n + 1] - p.cu_host[n]);
   }
-  const int64_t chunks = (longest + kC - 1) / kC;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(kSMs / walks, chunks / 4));
+  const int64_t chunks = (longest + kC - 1) / kC, most = std::min<int64_t>(kSMs / walks, chunks / 4);
+  return most >= 3 ? (int)most : 1;
 }
 
 int edge_parts(const LaProblem& p) { return p.dv / kNV * 8; }

