@@ -19,7 +19,8 @@
 //
 // Each thread loads its next row before it works on the present one. Measured: gated norm of 262144 x 128 bf16, forward 33 us
 // (6.1 TB/s of its inputs and outputs), backward 58 us (5.8); residual norm of 16384 x 2048, fp32 stream, forward
-// 58 us (6.9), backward 104 us (5.8). Odd widths move 2 or 4 bytes a thread at a time and reach about half of that.
+// 58 us (6.9), backward 104 us (5.8). At 33.5 M elements of other even widths the backwards reach 3.9 to 6.1 TB/s, 2.9 at 8192
+// columns; odd widths move 2 or 4 bytes a thread at a time and reach 2.1 to 4.5 TB/s.
 #include <initializer_list>
 #include <type_traits>
 
@@ -113,7 +114,9 @@ struct RowSum {
       if (lane == 0)
 #pragma unroll
         for (int m = 0; m < M; ++m) smem[slot][warp][m] = v[m];
-      __syncthreads();
+      // the row's own threads meet, not those of the CTA's other rows
+      if constexpr (TPR < 256) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+      else __syncthreads();
       constexpr int PER = TPR / 32;         // warps a row
       const int w0 = warp / PER * PER;
 #pragma unroll
@@ -317,9 +320,15 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
   __shared__ float red[RPC > 1 ? threads_of(TPR) * E : 1];
   int slot = 0;
   const int t = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  // 1024 threads have 64 registers each: the weights come from L1 for every row, and no row is fetched ahead (207 us
+  // at 4096 x 8192, fp32; with both, in spills, 267 us)
+  constexpr bool LEAN = TPR == 1024;
   float w1[E], w2[E], acc[2][E] = {};
-  load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
-  if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
+  auto weights = [&] {
+    load_w<TPR, VEC>(w_pre, w_bf16, D, t, w1);
+    if (POST) load_w<TPR, VEC>(w_post, w_bf16, D, t, w2);
+  };
+  if (!LEAN) weights();
   const float inv_d = 1.f / (float)D;
   Raw<TPR, VEC, __nv_bfloat16> ny, nd;
   Raw<TPR, VEC, H> nh, ndh;
@@ -332,20 +341,23 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
     nd.load(dx + q * D, in, D, t);
     ndh.load(dh_out + q * D, in && dh_out, D, t);
   };
-  load(r);
+  if (!LEAN) load(r);
   for (int64_t r0 = (int64_t)blockIdx.x * RPC; r0 < rows; r0 += stride, r += stride) {
     const bool live = r < rows;
     float yv[E], hv[E], dv[E], dhv[E];
+    if (LEAN) {
+      load(r);
+      weights();
+    }
     ny.get(yv);
     nh.get(hv);
     nd.get(dv);
     ndh.get(dhv);
-    load(r + stride);
+    if (!LEAN) load(r + stride);
     // With u = y w_post, p = dx w_pre, a = alpha r_y, h' = h + a u, all sums of the row are polynomials in a of
     // seven sums that need no other first: one reduction instead of three in a row.
-    constexpr bool ONE = POST && (TPR <= 32 || TPR >= 256);
     float ry = 1.f, ss, sp, su = 0.f, gu = 0.f, pu = 0.f;   // sums of h' h', p h', h' u, dh' u, p u
-    if (ONE) {
+    if (POST) {
       float s[7] = {};
 #pragma unroll
       for (int e = 0; e < E; ++e) {
@@ -385,17 +397,10 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
         su = x[2];
       }
     } else {
-      if (POST) {
-        float s[1] = {0.f};
-#pragma unroll
-        for (int e = 0; e < E; ++e) s[0] = fmaf(yv[e], yv[e], s[0]);
-        RowSum<TPR, 1>::run(s, sm, slot);
-        ry = rsqrtf(fmaf(s[0], inv_d, eps));
-      }
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        hv[e] = fmaf(alpha, POST ? yv[e] * ry * w2[e] : yv[e], hv[e]);
+        hv[e] = fmaf(alpha, yv[e], hv[e]);
         s[0] = fmaf(hv[e], hv[e], s[0]);
         s[1] = fmaf(dv[e] * w1[e], hv[e], s[1]);
       }
@@ -405,18 +410,14 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
     }
     const float rh = rsqrtf(fmaf(ss, inv_d, eps));
     const float c = sp * inv_d * rh * rh;
-    float q[1] = {0.f};
 #pragma unroll
     for (int e = 0; e < E; ++e) {
       acc[0][e] = fmaf(dv[e], hv[e] * rh, acc[0][e]);
       dhv[e] += rh * fmaf(-c, hv[e], dv[e] * w1[e]);
-      if (POST && !ONE) q[0] = fmaf(alpha * dhv[e] * w2[e], yv[e], q[0]);
     }
-    if (ONE) q[0] = alpha * (gu + rh * (pu - c * su));
     if (live) store_row<TPR, VEC>(dh + r * D, D, t, dhv);
     if (POST) {
-      if (!ONE) RowSum<TPR, 1>::run(q, sm, slot);
-      const float cy = q[0] * inv_d * ry * ry;
+      const float cy = alpha * (gu + rh * (pu - c * su)) * inv_d * ry * ry;   // mean(e w_post n) r_y
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float en = alpha * dhv[e];
