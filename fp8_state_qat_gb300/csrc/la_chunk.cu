@@ -25,8 +25,10 @@ struct DgParams {
   GateSrc gates;
   const float *rq, *rk, *aq, *bk;        // per (token, head): r and c in two parts, a, b
   int64_t th;                            // tokens x heads
-  const float* edge;                     // exp(gam_C) <S, dS> per item, in parts
+  const float* edge;                     // exp(gam_C) <S, dS> per item, in parts; or null:
   int parts;
+  const __nv_bfloat16 *S, *dS;           // then from the two terms of S and dS, per item
+  int elems;                             // of a state
   float* dg;                             // [tokens, Hv], or per item with head_decay
 };
 
@@ -51,8 +53,31 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
   }
   const int L = (int)(len - c * kC < kC ? len - c * kC : kC);
   __shared__ float red[3][4];
-  // exp(gam_C) <S, dS>, from its parts (at most 32)
-  float x = t < p.parts ? p.edge[item * p.parts + t] : 0.f;
+  // exp(gam_C) <S, dS>, from its parts (at most 32), or from S and dS
+  float x = 0.f;
+  if (p.edge) {
+    if (t < p.parts) x = p.edge[item * p.parts + t];
+  } else {
+    float gx[4];
+    Gates w;
+    p.gates.load(gx, tok, h, L, lane);
+    const uint4* S = reinterpret_cast<const uint4*>(p.S + 2 * item * p.elems);
+    const uint4* dS = reinterpret_cast<const uint4*>(p.dS + 2 * item * p.elems);
+    const int n = p.elems / 8;
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll 4
+    for (int i = t; i < n; i += kC) {
+      const uint4 a = S[i], al = S[i + n], b = dS[i], bl = dS[i + n];
+      const uint32_t au[4] = {a.x, a.y, a.z, a.w}, alu[4] = {al.x, al.y, al.z, al.w};
+      const uint32_t bu[4] = {b.x, b.y, b.z, b.w}, blu[4] = {bl.x, bl.y, bl.z, bl.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        s = __ffma2_rn(__fadd2_rn(unpack_bf16(au[q]), unpack_bf16(alu[q])),
+                       __fadd2_rn(unpack_bf16(bu[q]), unpack_bf16(blu[q])), s);
+    }
+    scan_gates(gx, w, lane);
+    x = warp_sum(s.x + s.y) * expf((w.tot(0) + w.tot(1)) + (w.tot(2) + w.tot(3)));
+  }
   const int64_t at = (tok + t) * Hv + h;
   float f = 0.f, b = 0.f;
   if (t < L) {
@@ -66,10 +91,10 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
     if (lane + off < 32) fs += yf;
     if (lane >= off) bs += yb;
   }
-  if (warp == 0) x = warp_sum(x);
+  if (p.edge) x = warp_sum(x);
   if (lane == 0) {
     red[0][warp] = fs;
-    if (warp == 0) red[2][0] = x;
+    red[2][warp] = x;
   }
   if (lane == 31) red[1][warp] = bs;
   __syncthreads();
@@ -79,7 +104,7 @@ __global__ void __launch_bounds__(kC) la_dg_kernel(const DgParams p) {
     if (w > warp) after += red[0][w];
     if (w < warp) before += red[1][w];
   }
-  v = (v + (after + before)) + red[2][0];
+  v = (v + (after + before)) + ((red[2][0] + red[2][1]) + (red[2][2] + red[2][3]));
   if (!p.gates.head_decay) {
     if (t < L) p.dg[at] = v;
     return;
@@ -150,7 +175,7 @@ Layout layout_of(const LaProblem& p, bool bwd) {
     l.rk = take(th * 8);
     l.aq = take(th * 4);
     l.bk = take(th * 4);
-    l.edge = take(items * edge_parts(p) * 4);
+    if (!walks_beside(p)) l.edge = take(items * edge_parts(p) * 4);
     if (p.Hv != p.Hqk) {
       l.pq = take(th * p.dk * 4);
       l.pk = take(th * p.dk * 4);
@@ -176,7 +201,7 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
   StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
-             nullptr, nullptr};
+             nullptr, nullptr, 0};
   // o reads h0 through the states alone, so hT may be h0
   if ((e = launch_states(p, s, status, false, stream)) != cudaSuccess) return e;
   // tiles k, q, v | S
@@ -195,11 +220,13 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   float *rq = (float*)(base + l.rq), *rk = (float*)(base + l.rk), *aq = (float*)(base + l.aq), *bk = (float*)(base + l.bk);
   float* const edge = (float*)(base + l.edge);
   float *pq = (float*)(base + l.pq), *pk = (float*)(base + l.pk);
+  const bool beside = walks_beside(p);
   cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
   if (e != cudaSuccess) return e;
-  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr};
+  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr, 0};
   if ((e = launch_states(p, f, status, false, stream)) != cudaSuccess) return e;
-  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec, base + l.S, edge};
+  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec,
+             beside ? nullptr : base + l.S, beside ? nullptr : edge, beside};
   if ((e = launch_states(p, b, status, true, stream)) != cudaSuccess) return e;
   if (tokens == 0 || items == 0)
     return p.head_decay ? cudaMemsetAsync(gr.dg, 0, (size_t)p.Hv * 4, stream) : cudaSuccess;
@@ -209,7 +236,8 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   o.role[1] = {0, 3, 1, 2, 2, 2, 0x21, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
   o.role[2] = {2, 1, 3, -1, 2, 1, 0x17, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
   if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
-  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, tokens * p.Hv, edge, edge_parts(p),
+  DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, tokens * p.Hv, beside ? nullptr : edge,
+             edge_parts(p), (const __nv_bfloat16*)(base + l.S), (const __nv_bfloat16*)(base + l.dS), p.dk * p.dv,
              p.head_decay ? (float*)(base + l.item) : gr.dg};
   if ((e = launch(true, la_dg_kernel, dim3((unsigned)items), kC, 0, stream, d)) != cudaSuccess) return e;
   if (p.head_decay) {

@@ -231,9 +231,11 @@ struct StateRun {
   float* seg_dec;       // [N Hv][nseg]
   const void* other;    // two-term states S of the chunks, or null: then exp(gam_C) <S, state before the chunk>
   float* edge;          // per item goes here, in edge_parts() parts
+  int beside;           // the launch before it may still run: nothing that it writes is read
 };
 int edge_parts(const LaProblem& p);
 int state_segments(const LaProblem& p);
+bool walks_beside(const LaProblem& p);
 // dependent: the launch before it in the stream is one of these kernels
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream);
 

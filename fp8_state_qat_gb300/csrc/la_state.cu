@@ -50,6 +50,7 @@ struct Params {
   int store, other; // the states are stored; <S, state> is computed
   int sets;         // of V's terms: 2, or 1 where S needs the room
   float scale;
+  int beside;       // the kernel before this one need only be done when this one is
   int sorted;
   uint8_t order[64];   // the sequences, longest first
 };
@@ -155,7 +156,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   bool ok = true;
   // inputs of the call are read above and below without waiting; what a kernel of this call wrote (the joined
   // segment states, S) and what it may still read (the workspace) only after
-  dependency_wait();
+  if (!p.beside) dependency_wait();
 
   float s[kHC];   // state elements (row, vt kNV + part kHC + j)
   const int64_t sbase_g = ((int64_t)unit * p.dk + row) * p.dv + vt * kNV + part * kHC;
@@ -412,6 +413,7 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
   __syncthreads();
   tc::tc_fence_after();
   if (warp == 0) tc::tmem_dealloc(tmem, kTmemCols);
+  if (p.beside) dependency_wait();   // what comes next waits for this kernel alone
   if (sh.dead) return;
   if (warp >= 8) {
     if (p.totals && tid == 256 && vt == 0) p.seg_dec[unit * p.nseg + seg] = expf(sh.log_decay[0] + sh.log_decay[1]);
@@ -474,6 +476,14 @@ int state_segments(const LaProblem& p) {
   return most >= 3 ? (int)most : 1;
 }
 
+// Few walks leave room for the backwards walk beside the forwards one: it then starts with it, and <S, dS>, which
+// it would take from the stored S on its way, is left to the dg kernel. A training step at 5 packed sequences of 1 to
+// 1000 tokens, 4 heads (40 CTAs): 79 -> 68 us; 3 x 1000 tokens, 8 heads, d 64 (24): 87 -> 74; 2 x 2048, 18 heads, d 128
+// (72): 177 -> 175; at 4 x 1024, 16 heads (128, of which 24 find a free SM): 143 -> 168, so only where all have one.
+bool walks_beside(const LaProblem& p) {
+  return state_segments(p) == 1 && 2 * (int64_t)p.N * p.Hv * (p.dv / kNV) <= kSMs;
+}
+
 int edge_parts(const LaProblem& p) { return p.dv / kNV * 8; }
 
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream) {
@@ -494,7 +504,7 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bo
   if (r.other && !make_bf16_rows_map(&m[3], r.other, rows * 2, p.dk)) return cudaErrorNotSupported;
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
            status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
-           r.other ? 1 : 2, r.scale};
+           r.other ? 1 : 2, r.scale, r.beside};
   // Walks of unequal lengths: the longest first, so that the last ones to start are short (b = 1, 8 packed
   // sequences of 1 to 8192 tokens, 32 heads: an eighth of the time). Many sequences even out by themselves.
   if (p.cu_host && p.N <= 64) {
