@@ -133,6 +133,13 @@ __global__ void __launch_bounds__(256) la_dg_head_kernel(const float* part, floa
   if (t == 0) dg[h] = (float)red[0];
 }
 
+// The status word. Cleared by a kernel, the walk after it sets itself up meanwhile: a forward of 1 x 256 tokens, 2 heads
+// 16.2 us with a memset in its place, 14.6 us with this; in a CUDA graph 15.8 and 12.9.
+__global__ void la_clear_kernel(int* status) {
+  dependents_may_start();
+  *status = 0;
+}
+
 // dq and dk (blockIdx.y) of a shared head: the sum over its value heads, four channels a thread
 __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, const float* x1, __nv_bfloat16* y0,
                                                            __nv_bfloat16* y1, int64_t quads, int G, int D4) {
@@ -198,12 +205,12 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
   unsigned char* const base = static_cast<unsigned char*>(ws);
   const Layout l = layout_of(p, false);
   int* const status = static_cast<int*>(ws);
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
+  cudaError_t e = launch(false, la_clear_kernel, dim3(1), 1, 0, stream, status);
   if (e != cudaSuccess) return e;
   StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
              nullptr, nullptr, 0};
   // o reads h0 through the states alone, so hT may be h0
-  if ((e = launch_states(p, s, status, false, stream)) != cudaSuccess) return e;
+  if ((e = launch_states(p, s, status, true, stream)) != cudaSuccess) return e;
   // tiles k, q, v | S
   OutRun o{{p.q, p.k, p.v, nullptr}, {base + l.S, nullptr}, {1, 1}, 3, {1, 0, 2, 0}, 1, {0}, {0}, {}, 1};
   o.role[0] = {1, 0, 2, -1, 0, 1, 0x17, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
@@ -221,10 +228,11 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   float* const edge = (float*)(base + l.edge);
   float *pq = (float*)(base + l.pq), *pk = (float*)(base + l.pk);
   const bool beside = walks_beside(p);
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), stream);
+  cudaError_t e = launch(false, la_clear_kernel, dim3(1), 1, 0, stream, status);
   if (e != cudaSuccess) return e;
   StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr, 0};
-  if ((e = launch_states(p, f, status, false, stream)) != cudaSuccess) return e;
+  // a walk that the next one may overtake starts when the status word is clear
+  if ((e = launch_states(p, f, status, !beside, stream)) != cudaSuccess) return e;
   StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec,
              beside ? nullptr : base + l.S, beside ? nullptr : edge, beside};
   if ((e = launch_states(p, b, status, true, stream)) != cudaSuccess) return e;
