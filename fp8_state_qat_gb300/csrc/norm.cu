@@ -20,8 +20,8 @@
 //
 // Each thread loads its next row before it works on the present one. Measured: gated norm of 262144 x 128 bf16, forward 33 us
 // (6.1 TB/s of its inputs and outputs), backward 58 us (5.8); residual norm of 16384 x 2048, fp32 stream, forward
-// 58 us (6.9), backward 104 us (5.8). At 33.5 M elements of other even widths the backwards reach 3.9 to 6.1 TB/s, 2.9 at 8192
-// columns; odd widths move 2 or 4 bytes a thread at a time and reach 2.1 to 4.5 TB/s.
+// 58 us (6.9), backward 90 us (6.7). At 33.5 M elements of other even widths the backwards reach 3.9 to 6.2 TB/s, 2.8 to 3.9 at
+// 8192 columns; odd widths move 2 or 4 bytes a thread at a time and reach 2.5 to 5.3 TB/s.
 #include <initializer_list>
 #include <type_traits>
 
@@ -94,7 +94,7 @@ __device__ __forceinline__ void load_w(const void* w, int w_bf16, int D, int t, 
   else load_row<TPR, VEC>(static_cast<const float*>(w), D, t, v);
 }
 
-constexpr int kSums = 7;               // values that one reduction sums at most
+constexpr int kSums = 8;               // places for the values that one reduction sums
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 // Resident CTAs an SM that a backward's registers leave room for (and its launch asks for): its rows in flight
 // need about 100 registers a thread.
@@ -106,6 +106,10 @@ template <int TPR, int M>
 struct RowSum {
   static constexpr int kWarps = threads_of(TPR) / 32;
   static __device__ __forceinline__ void run(float (&v)[M], float (*smem)[kWarps][kSums], int& slot) {
+    if constexpr (M > 4) many(v, smem, slot);
+    else each(v, smem, slot);
+  }
+  static __device__ __forceinline__ void each(float (&v)[M], float (*smem)[kWarps][kSums], int& slot) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
     for (int m = 0; m < M; ++m)
@@ -116,9 +120,7 @@ struct RowSum {
       if (lane == 0)
 #pragma unroll
         for (int m = 0; m < M; ++m) smem[slot][warp][m] = v[m];
-      // the row's own threads meet, not those of the CTA's other rows
-      if constexpr (TPR < 256) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
-      else __syncthreads();
+      meet();
       constexpr int PER = TPR / 32;         // warps a row
       const int w0 = warp / PER * PER;
 #pragma unroll
@@ -130,6 +132,53 @@ struct RowSum {
       }
       slot ^= 1;
     }
+  }
+  // 5 to 8 values: the first three exchanges halve the values that a lane keeps, so that lane l ends with the sum of
+  // value l / (W / 8) alone; then everyone reads all of them. 18 shuffles for 7 values of 8 warps, where a tree for each
+  // value takes 63, and half of the time went to them (residual backward of 33.5 M elements, 1024 columns, bf16 103 ->
+  // 78 us, fp32 141 -> 103; 2048 columns 103 -> 78, 110 -> 98).
+  static __device__ __forceinline__ void many(float (&v)[M], float (*smem)[kWarps][kSums], int& slot) {
+    constexpr int W = TPR < 32 ? TPR : 32, G = W / 8;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float a[8];
+#pragma unroll
+    for (int m = 0; m < 8; ++m) a[m] = m < M ? v[m] : 0.f;
+#pragma unroll
+    for (int n = 4; n > 0; n >>= 1) {   // lanes o apart share 2 n values, the upper one keeps the upper n
+      const int o = n * G;
+      const bool upper = lane & o;
+#pragma unroll
+      for (int m = 0; m < n; ++m) {
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? a[m] : a[m + n], o);
+        a[m] = (upper ? a[m + n] : a[m]) + other;
+      }
+    }
+    float s = a[0];
+#pragma unroll
+    for (int o = G / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if constexpr (TPR <= 32) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) v[m] = __shfl_sync(0xffffffffu, s, m * G, W);
+    } else {
+      if (lane % G == 0) smem[slot][warp][lane / G] = s;
+      meet();
+      constexpr int PER = TPR / 32;
+      const int w0 = warp / PER * PER, m = lane & 7;
+      s = 0.f;
+#pragma unroll
+      for (int w = 0; w < PER; w += 4)
+        if (w + (lane >> 3) < PER) s += smem[slot][w0 + w + (lane >> 3)][m];
+      s += __shfl_xor_sync(0xffffffffu, s, 8);
+      s += __shfl_xor_sync(0xffffffffu, s, 16);
+#pragma unroll
+      for (int j = 0; j < M; ++j) v[j] = __shfl_sync(0xffffffffu, s, j);
+      slot ^= 1;
+    }
+  }
+  // the row's own threads meet, not those of the CTA's other rows
+  static __device__ __forceinline__ void meet() {
+    if constexpr (TPR < 256) asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.x / TPR), "n"(TPR) : "memory");
+    else __syncthreads();
   }
 };
 
