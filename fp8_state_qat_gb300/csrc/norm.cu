@@ -21,7 +21,7 @@
 // Each thread loads its next row before it works on the present one. Measured: gated norm of 262144 x 128 bf16, forward 33 us
 // (6.1 TB/s of its inputs and outputs), backward 58 us (5.8); residual norm of 16384 x 2048, fp32 stream, forward
 // 58 us (6.9), backward 90 us (6.7). At 33.5 M elements of other even widths the backwards reach 3.9 to 6.2 TB/s, 2.8 to 3.9 at
-// 8192 columns; odd widths move 2 or 4 bytes a thread at a time and reach 2.5 to 5.3 TB/s.
+// 8192 columns; odd widths move 2 or 4 bytes a thread at a time and reach 2.0 to 5.7 TB/s.
 #include <initializer_list>
 #include <type_traits>
 
