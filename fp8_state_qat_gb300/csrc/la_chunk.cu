@@ -171,7 +171,7 @@ Layout layout_of(const LaProblem& p, bool bwd) {
     at += up(n);
     return here;
   };
-  l.S = take(items * elems * 2 * (bwd ? 2 : 1));
+  l.S = take(items * elems * 4);
   if (bwd) l.dS = take(items * elems * 4);
   if (nseg > 1) {
     l.tot = take((size_t)p.N * p.Hv * nseg * elems * 4);
@@ -207,13 +207,13 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream) {
   int* const status = static_cast<int*>(ws);
   cudaError_t e = launch(false, la_clear_kernel, dim3(1), 1, 0, stream, status);
   if (e != cudaSuccess) return e;
-  StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 1, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
+  StateRun s{p.k, p.v, p.h0, p.hT, base + l.S, 0, 1.f, (float*)(base + l.tot), (float*)(base + l.dec),
              nullptr, nullptr, 0};
   // o reads h0 through the states alone, so hT may be h0
   if ((e = launch_states(p, s, status, true, stream)) != cudaSuccess) return e;
-  // tiles k, q, v | S
-  OutRun o{{p.q, p.k, p.v, nullptr}, {base + l.S, nullptr}, {1, 1}, 3, {1, 0, 2, 0}, 1, {0}, {0}, {}, 1};
-  o.role[0] = {1, 0, 2, -1, 0, 1, 0x17, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
+  // tiles k, q, v | S hi, lo
+  OutRun o{{p.q, p.k, p.v, nullptr}, {base + l.S, nullptr}, 3, {1, 0, 2, 0}, 2, {0, 0}, {0, 1}, {}, 1};
+  o.role[0] = {1, 0, 2, -1, 0, 0x37, 0, 0, p.scale, p.scale, p.o, 0, nullptr, nullptr};
   return launch_outputs(p, o, status, stream);
 }
 
@@ -230,19 +230,19 @@ cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaS
   const bool beside = walks_beside(p);
   cudaError_t e = launch(false, la_clear_kernel, dim3(1), 1, 0, stream, status);
   if (e != cudaSuccess) return e;
-  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 2, 0, 1.f, tot, dec, nullptr, nullptr, 0};
+  StateRun f{p.k, p.v, p.h0, nullptr, base + l.S, 0, 1.f, tot, dec, nullptr, nullptr, 0};
   // a walk that the next one may overtake starts when the status word is clear
   if ((e = launch_states(p, f, status, !beside, stream)) != cudaSuccess) return e;
-  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 2, 1, p.scale, tot, dec,
+  StateRun b{p.q, gr.dout, gr.dhT, gr.dh0, base + l.dS, 1, p.scale, tot, dec,
              beside ? nullptr : base + l.S, beside ? nullptr : edge, beside};
   if ((e = launch_states(p, b, status, true, stream)) != cudaSuccess) return e;
   if (tokens == 0 || items == 0)
     return p.head_decay ? cudaMemsetAsync(gr.dg, 0, (size_t)p.Hv * 4, stream) : cudaSuccess;
   // tiles v, q, k, do | S hi, lo, dS hi, lo
-  OutRun o{{p.q, p.k, p.v, gr.dout}, {base + l.S, base + l.dS}, {2, 2}, 4, {2, 0, 1, 3}, 4, {0, 0, 1, 1}, {0, 1, 0, 1}, {}, 3};
-  o.role[0] = {3, 0, 2, 1, 0, 2, 0x30, 1, 0, p.scale, p.scale, G > 1 ? (void*)pq : gr.dq, G > 1, rq, aq};
-  o.role[1] = {0, 3, 1, 2, 2, 2, 0x21, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
-  o.role[2] = {2, 1, 3, -1, 2, 1, 0x17, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
+  OutRun o{{p.q, p.k, p.v, gr.dout}, {base + l.S, base + l.dS}, 4, {2, 0, 1, 3}, 4, {0, 0, 1, 1}, {0, 1, 0, 1}, {}, 3};
+  o.role[0] = {3, 0, 2, 1, 0, 0x30, 1, 0, p.scale, p.scale, G > 1 ? (void*)pq : gr.dq, G > 1, rq, aq};
+  o.role[1] = {0, 3, 1, 2, 2, 0x01, 1, 1, p.scale, 1.f, G > 1 ? (void*)pk : gr.dk, G > 1, rk, bk};
+  o.role[2] = {2, 1, 3, -1, 2, 0x37, 0, 1, p.scale, 1.f, gr.dv, 0, nullptr, nullptr};
   if ((e = launch_outputs(p, o, status, stream)) != cudaSuccess) return e;
   DgParams d{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, rq, rk, aq, bk, tokens * p.Hv, beside ? nullptr : edge,
              edge_parts(p), (const __nv_bfloat16*)(base + l.S), (const __nv_bfloat16*)(base + l.dS), p.dk * p.dv,

@@ -195,19 +195,18 @@ inline cudaError_t allow_smem(K kernel, uint32_t bytes, std::atomic<uint64_t>& d
 }
 
 // ---- launchers of the parts (la_state.cu, la_out.cu) ----
-// States at chunk boundaries, bf16 terms per item = slot * Hv + h: [term][dv / 64][dk][64].
+// States at chunk boundaries, two bf16 terms (hi, lo) per item = slot * Hv + h: [term][dv / 64][dk][64].
 struct StateRun {
   const void* x;        // bf16 [tokens, Hqk, dk]: k forwards, q backwards
   const void* y;        // bf16 [tokens, Hv, dv]: v forwards, dout backwards
   const float* s0;      // [N, Hv, dk, dv] or null
   float* sT;            // [N, Hv, dk, dv] or null
   void* states;         // the state before each chunk's own contribution, or null
-  int terms;            // bf16 terms stored: 1 (rounded) or 2 (hi + lo)
   int reverse;
   float scale;          // weight of every token's contribution
   float* seg_tot;       // split walks: [N Hv][nseg][dk][dv]
   float* seg_dec;       // [N Hv][nseg]
-  const void* other;    // two-term states S of the chunks, or null: then exp(gam_C) <S, state before the chunk>
+  const void* other;    // the states S of the chunks, or null: then exp(gam_C) <S, state before the chunk>
   float* edge;          // per item goes here, in edge_parts() parts
   int beside;           // the launch before it may still run: nothing that it writes is read
 };
@@ -222,7 +221,7 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bo
 // The operands are tiles of the chunk, by their places in OutRun's lists.
 struct Role {
   int a, b, c, e;        // token tiles; e: rows dotted with the outputs, or -1
-  int st, terms;         // first state tile and the terms of the state that are used
+  int st;                // first of the two tiles of the state's terms
   int done;              // tiles that no later role of the chunk reads: bits 0-2 a, b, c; bits 4, 5 the state terms
   int st_transposed;     // St = S^T: the product is over the value columns
   int reverse;
@@ -235,7 +234,6 @@ struct Role {
 struct OutRun {
   const void* tensor[4]; // q, k, v, dout
   const void* states[2]; // S, dS
-  int terms[2];
   int ntok, tok[4];      // token tiles of a chunk, in the order of their release: which tensor
   int nst, st[4], term[4];   // state tiles: which states, which term
   Role role[3];

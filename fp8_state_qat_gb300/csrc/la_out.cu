@@ -8,16 +8,18 @@
 //   dv: a = k,  b = q,  c = do, St = dS (leaving the chunk)      s >= t, D = exp(gam_s - gam_t), E = exp(gam_C - gam_t)
 //   dk: a = v,  b = do, c = q,  St = dS^T                        likewise
 // and per item (chunk, value head, role) three tcgen05 products with M = 128 tokens:
-//   scores a b^T -> weighted by D and the mask, rounded to bf16, back into tensor memory as an A operand;
+//   scores a b^T -> weighted by D and the mask, in two bf16 terms back into tensor memory as A operands;
 //   a St into an accumulator of its own (its row weights E differ from the scores');  P c.
 // The roles dq and dk also give the parts of dg, sums over pairs of tokens of
 // D (a_t . b_s) (e_t . c_s) with e = q or k: those take a fourth product e c^T and fp32 sums before any
 // rounding, and e_t . (a_t^T St) with the state in two bf16 terms.
 //
-// Roundings to bf16: the weighted scores and the state, each once, against outputs that are bf16
-// themselves; everything else is fp32.
+// The weighted scores and the states are each a sum of two bf16 terms (16 bits and a sign: 2^-18 of the value), so
+// that the outputs' own rounding to bf16 is the only one that shows: o, dq, dk, dv are off by 1.7e-3 of 64 bits, as
+// their rounded values are; with one term of each it was 2.3e-3. dg is fp32 and rests on the same two-term states:
+// they leave it 1e-6 to 3e-6 off where the states carry much of it. A third term would be 32 KB more a chunk and state.
 //
-// What bounds it is the traffic: 3 or 4 token tiles and 1 to 4 state terms in (32 KB each at d = 128), one tile out a
+// What bounds it is the traffic: 3 or 4 token tiles and 2 or 4 state terms in (32 KB each at d = 128), one tile out a
 // role. So one persistent CTA per SM keeps six 32 KB tiles filled ahead by TMA, across items; the three roles of a
 // chunk follow each other on the same token tiles; one warp issues the products; one computes the decays an
 // item ahead; eight weight the scores; four write the outputs of an item while the others go on to the next. The
@@ -48,7 +50,6 @@ struct Params {
   GateSrc gates;
   Role role[3];
   int heads[4], width[4];   // of q, k, v, do
-  int terms[2];
   int ntok, tok[4], nst, st[4], term[4];
   int* status;
   int64_t dot_stride;       // between the two halves of dot_in
@@ -182,7 +183,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
           tc::mbar_expect_tx(bar, D / 64 * kBlk);
           for (int b = 0; b < D / 64; ++b) tc::tma_load_3d(dst + b * kBlk, &maps.t[m], bar, 64 * b, hh, it.tok);
         } else {
-          const int w = p.st[j], row = (it.state * p.terms[w] + p.term[j]) * p.dk * (p.dv / 64);
+          const int w = p.st[j], row = (it.state * 2 + p.term[j]) * p.dk * (p.dv / 64);
           tc::mbar_expect_tx(bar, p.dk * p.dv * 2);
           for (int b = 0; b < p.dv / 64; ++b) tc::tma_load_2d(dst + b * p.dk * 128, &maps.s[w], bar, 0, row + b * p.dk);
         }
@@ -328,7 +329,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       }
       mma_commit_w(tc::smem_u32(&sh.sc), me);
       slanded(r.st);
-      if (r.terms > 1) slanded(r.st + 1);
+      slanded(r.st + 1);
       if (k > 0) ok = ok && wait(sh.dead, sh.ofree, (k - 1) & 1);
       if (!good()) break;
       tc::tc_fence_after();
@@ -341,7 +342,7 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       const uint32_t kblk = r.st_transposed ? sblk : 8192;
       const uint64_t ad = tc::make_sdesc(ttile(r.a), 16, 1024);
 #pragma unroll 1
-      for (int t = 0; t < r.terms; ++t) {
+      for (int t = 0; t < 2; ++t) {
         const uint64_t bd = tc::make_sdesc(stile(r.st + t), lbo, 1024);
 #pragma unroll 1
         for (int b = 0; b < na; ++b)
@@ -359,9 +360,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
       {
         const uint64_t bd = tc::make_sdesc(ttile(r.c), kBlk, 1024);
         const uint32_t idesc = tc::make_idesc(tc::kKindBF16, 128, 64 * nc, false, true);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t)   // P's terms: 16 columns each of a block's 32
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          mma_bf16_ta(tmem + TM_O, tmem + TM_S + 8 * ks + (ks & 4) * 8, dadv(bd, ks * 2048), idesc, ks > 0, me);
+          for (int ks = 0; ks < 8; ++ks)
+            mma_bf16_ta(tmem + TM_O, tmem + TM_S + 16 * t + 32 * (ks >> 1) + 8 * (ks & 1), dadv(bd, ks * 2048), idesc,
+                        t + ks > 0, me);
         if (r.done & 4) trelease(r.c);
         mma_commit_w(tc::smem_u32(&sh.oo), me);
       }
@@ -403,11 +407,12 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
 #pragma unroll 1
       for (int j = 2 * half; j < 2 * half + 2; ++j) {
         uint32_t u[16];
-        const uint32_t pcol = TM_S + 64 * half + 16 * (j & 1);   // over scores that this warp alone reads, before
+        const uint32_t pcol = tc::tmem_addr(tmem, lane0, TM_S + 32 * j);   // P's terms over the block's own scores
         if (rev ? j < w : j > w) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) u[c] = 0;
-          tmem_st16u(tc::tmem_addr(tmem, lane0, pcol), u);
+          tmem_st16u(pcol, u);
+          tmem_st16u(pcol + 16, u);
           continue;
         }
         const bool diag = j == w;
@@ -448,7 +453,13 @@ la_out_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params 
         }
 #pragma unroll
         for (int c = 0; c < 16; ++c) u[c] = pack_bf16(v[2 * c], v[2 * c + 1]);
-        tmem_st16u(tc::tmem_addr(tmem, lane0, pcol), u);
+        tmem_st16u(pcol, u);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float2 low = __ffma2_rn(unpack_bf16(u[c]), make_float2(-1.f, -1.f), make_float2(v[2 * c], v[2 * c + 1]));
+          u[c] = pack_bf16(low.x, low.y);
+        }
+        tmem_st16u(pcol + 16, u);
         if (dg) {
           if (diag) mask &= ~(1u << lane);   // pairs of different tokens
           float ev[32];
@@ -606,9 +617,8 @@ cudaError_t launch_outputs(const LaProblem& p, const OutRun& r, int* status, cud
     else if (!make_bf16_map(&m.t[i], r.tensor[i], width[i], heads[i], tokens, kC)) return cudaErrorNotSupported;
   }
   for (int i = 0; i < 2; ++i) {
-    o.terms[i] = r.terms[i];
     if (!r.states[i]) m.s[i] = m.s[0];   // not used
-    else if (!make_bf16_rows_map(&m.s[i], r.states[i], slots * p.Hv * r.terms[i] * p.dk * (p.dv / 64), p.dk))
+    else if (!make_bf16_rows_map(&m.s[i], r.states[i], slots * p.Hv * 2 * p.dk * (p.dv / 64), p.dk))
       return cudaErrorNotSupported;
   }
   o.dot_stride = tokens * p.Hv;

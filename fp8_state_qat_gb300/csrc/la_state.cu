@@ -45,7 +45,7 @@ struct Params {
   float *seg_tot, *seg_dec;
   float* edge;
   int* status;
-  int Hqk, dk, dv, terms, reverse, nseg;
+  int Hqk, dk, dv, reverse, nseg;
   int totals;       // this launch computes the segments' contributions
   int store, other; // the states are stored; <S, state> is computed
   int sets;         // of V's terms: 2, or 1 where S needs the room
@@ -55,7 +55,7 @@ struct Params {
   uint8_t order[64];   // the sequences, longest first
 };
 __host__ __device__ inline uint32_t off_out(const Params& p) { return kOffTerm + p.sets * kTermSet; }
-__host__ __device__ inline uint32_t off_other(const Params& p) { return off_out(p) + (p.store ? p.terms * kBlk : 0); }
+__host__ __device__ inline uint32_t off_other(const Params& p) { return off_out(p) + (p.store ? 2 * kBlk : 0); }
 inline uint32_t smem_bytes(const Params& p) { return off_other(p) + (p.other ? 2 * kBlk : 0) + 1024; }
 constexpr uint32_t kMaxSmem = kOffTerm + 2 * kTermSet + 2 * kBlk + 1024;
 
@@ -222,14 +222,14 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
     }
   } else if (warp == 19) {
     // ---- states out, S in ----
-    auto state_row = [&](int i, int terms, int term) {   // of the stored states: this value tile's rows
+    auto state_row = [&](int i, int term) {   // of the stored states: this value tile's rows
       const int item = (slot0 + chunk_of(i)) * Hv + h;
-      return ((item * terms + term) * tiles + vt) * p.dk;
+      return ((item * 2 + term) * tiles + vt) * p.dk;
     };
     auto load_other = [&](int i) {
       tc::mbar_expect_tx(tc::smem_u32(&sh.ofull), 2 * p.dk * 128);
       for (int t = 0; t < 2; ++t)
-        tc::tma_load_2d(sbase + off_other(p) + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, 2, t));
+        tc::tma_load_2d(sbase + off_other(p) + t * kBlk, &to, tc::smem_u32(&sh.ofull), 0, state_row(i, t));
     };
     int os = 0;
     if (p.other && steps) {
@@ -241,8 +241,8 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
       ok = wait(sh.dead, sh.sready, i & 1);
       if (!(ok = __all_sync(0xffffffffu, ok))) break;
       if (lane == 0) {
-        for (int t = 0; t < p.terms; ++t)
-          tc::tma_store_2d(&ts, sbase + off_out(p) + t * kBlk, 0, state_row(i, p.terms, t));
+        for (int t = 0; t < 2; ++t)
+          tc::tma_store_2d(&ts, sbase + off_out(p) + t * kBlk, 0, state_row(i, t));
         tc::bulk_commit();
       }
       __syncwarp();
@@ -343,14 +343,10 @@ la_state_kernel(const __grid_constant__ CUtensorMap tx, const __grid_constant__ 
 #pragma unroll
           for (int j = 0; j < kHC; j += 8) {
             unsigned char* at = sm + off_out(p) + tc::sw128(row, (part * kHC + j) * 2);
-            if (p.terms == 2) {
-              uint4 hi, lo;
-              split8(s + j, hi, lo);
-              *reinterpret_cast<uint4*>(at) = hi;
-              *reinterpret_cast<uint4*>(at + kBlk) = lo;
-            } else {
-              *reinterpret_cast<uint4*>(at) = pack8(s + j);
-            }
+            uint4 hi, lo;
+            split8(s + j, hi, lo);
+            *reinterpret_cast<uint4*>(at) = hi;
+            *reinterpret_cast<uint4*>(at + kBlk) = lo;
           }
           tc::fence_proxy_async_smem();
         }
@@ -500,10 +496,10 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bo
     return cudaErrorNotSupported;
   m[2] = m[3] = m[0];   // where not used
   const int64_t rows = la_slots(p) * p.Hv * p.dk * (p.dv / 64);   // of one term
-  if (r.states && !make_bf16_rows_map(&m[2], r.states, rows * r.terms, p.dk)) return cudaErrorNotSupported;
+  if (r.states && !make_bf16_rows_map(&m[2], r.states, rows * 2, p.dk)) return cudaErrorNotSupported;
   if (r.other && !make_bf16_rows_map(&m[3], r.other, rows * 2, p.dk)) return cudaErrorNotSupported;
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
-           status, p.Hqk, p.dk, p.dv, r.terms, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
+           status, p.Hqk, p.dk, p.dv, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
            r.other ? 1 : 2, r.scale, r.beside};
   // Walks of unequal lengths: the longest first, so that the last ones to start are short (b = 1, 8 packed
   // sequences of 1 to 8192 tokens, 32 heads: an eighth of the time). Many sequences even out by themselves.
