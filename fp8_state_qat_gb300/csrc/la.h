@@ -39,6 +39,8 @@ cudaError_t launch_la_fwd(const LaProblem& p, void* ws, cudaStream_t stream);
 size_t la_bwd_workspace(const LaProblem& p);
 cudaError_t launch_la_bwd(const LaProblem& p, const LaGrads& gr, void* ws, cudaStream_t stream);
 
+cudaError_t launch_upload_i32(const int32_t* host, int32_t* device, int64_t n, cudaStream_t stream);
+
 cudaError_t launch_la_decode(const void* q, const void* k, const void* v, const float* g, const float* state,
                              float* state_out, void* o, int N, int Hqk, int Hv, int dk, int dv, float scale,
                              int state_qdq, cudaStream_t stream);

@@ -140,6 +140,18 @@ __global__ void la_clear_kernel(int* status) {
   *status = 0;
 }
 
+// Host values to device memory as launch parameters (4 KB hold 1000 of them). A copy would read the host's memory when
+// the stream comes to it, if that is pinned, or at a replay: offsets of packed sequences have to be those that the call's
+// sizes were made of.
+struct Values {
+  static constexpr int kMost = 1000;
+  int32_t v[kMost];
+};
+__global__ void __launch_bounds__(128) upload_kernel(const __grid_constant__ Values x, int32_t* device, int n) {
+  const int i = blockIdx.x * 128 + threadIdx.x;
+  if (i < n) device[i] = x.v[i];
+}
+
 // dq and dk (blockIdx.y) of a shared head: the sum over its value heads, four channels a thread
 __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, const float* x1, __nv_bfloat16* y0,
                                                            __nv_bfloat16* y1, int64_t quads, int G, int D4) {
@@ -197,6 +209,18 @@ Layout layout_of(const LaProblem& p, bool bwd) {
 }  // namespace la
 
 using namespace la;
+
+cudaError_t launch_upload_i32(const int32_t* host, int32_t* device, int64_t n, cudaStream_t stream) {
+  Values x;
+  for (int64_t at = 0; at < n; at += Values::kMost) {
+    const int m = (int)std::min<int64_t>(n - at, Values::kMost);
+    std::copy(host + at, host + at + m, x.v);
+    std::fill(x.v + m, x.v + Values::kMost, 0);
+    const cudaError_t e = launch(false, upload_kernel, dim3((unsigned)((m + 127) / 128)), 128, 0, stream, x, device + at, m);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 size_t la_fwd_workspace(const LaProblem& p) { return layout_of(p, false).total; }
 size_t la_bwd_workspace(const LaProblem& p) { return layout_of(p, true).total; }

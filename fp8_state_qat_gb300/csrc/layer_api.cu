@@ -92,6 +92,12 @@ gdn_status norm_sizes(int64_t rows, int32_t D, int32_t t, int32_t tw, float eps)
 
 extern "C" {
 
+gdn_status gdn_upload_i32(const int32_t* host, int32_t* device, int64_t n, gdn_stream_t stream) {
+  if (n < 0 || (n > 0 && (!host || !device)) || !aligned(host, 4) || !aligned(device, 4)) return GDN_ERR_INVALID_ARG;
+  const gdn_status s = gdn::check_device();
+  return s != GDN_OK ? s : done(gdn::launch_upload_i32(host, device, n, (cudaStream_t)stream));
+}
+
 size_t la_chunk_fwd_workspace_size(const la_chunk_args* args) {
   return validate_la_sizes(args) == GDN_OK ? gdn::la_fwd_workspace(problem_of(args)) : 0;
 }

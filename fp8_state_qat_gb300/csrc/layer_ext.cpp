@@ -8,6 +8,7 @@
 #include <cstdarg>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
@@ -26,8 +27,8 @@ using at::Tensor;
 // ---- the library's entry points, and the Python function that raises its errors ----
 #define ENTRIES(X)                                                                                                 \
   X(la_chunk_fwd) X(la_chunk_fwd_workspace_size) X(la_chunk_bwd) X(la_chunk_bwd_workspace_size) X(la_decode_step) \
-  X(gated_norm_fwd) X(gated_norm_bwd) X(gated_norm_bwd_workspace_size) X(residual_norm_fwd) X(residual_norm_bwd)  \
-  X(residual_norm_bwd_workspace_size)
+  X(gdn_upload_i32) X(gated_norm_fwd) X(gated_norm_bwd) X(gated_norm_bwd_workspace_size) X(residual_norm_fwd)     \
+  X(residual_norm_bwd) X(residual_norm_bwd_workspace_size)
 #define DECLARE(f) decltype(&::f) p_##f = nullptr;
 ENTRIES(DECLARE)
 #undef DECLARE
@@ -135,9 +136,28 @@ PyObject* pack(std::initializer_list<PyObject*> items) {   // steals the referen
 // ---- linear attention ----
 struct LaCall {
   la_chunk_args a{};
-  Tensor q, k, v, g, h0, cu_host, cu_dev;   // what the arguments point into
+  Tensor q, k, v, g, h0, cu_dev;   // what the arguments point into
+  std::vector<int32_t> cu_host;
   int device;
 };
+// The offsets of packed sequences, read once: the host's validation and sizes and the kernels go by the same values,
+// whatever becomes of the tensor after the call.
+void offsets(LaCall& c, const Tensor& cu) {
+  if (cu.dim() != 1 || cu.numel() < 1) bad(PyExc_ValueError, "cu_seqlens must be [N + 1]");
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cu.is_cuda() && cudaStreamIsCapturing((cudaStream_t)stream(c.device), &capture) == cudaSuccess &&
+      capture != cudaStreamCaptureStatusNone)
+    bad(PyExc_ValueError, "cu_seqlens on the device cannot be read while a graph is captured: pass a CPU tensor");
+  const Tensor host = cu.detach().to(at::kCPU, at::kLong).contiguous();
+  const int64_t* x = static_cast<const int64_t*>(host.data_ptr());
+  c.cu_host.resize((size_t)host.numel());
+  for (size_t i = 0; i < c.cu_host.size(); ++i) c.cu_host[i] = (int32_t)x[i];
+  c.cu_dev = make({host.numel()}, at::kInt, c.device);
+  int32_t* const device = static_cast<int32_t*>(c.cu_dev.data_ptr());
+  done("gdn_upload_i32", p_gdn_upload_i32(c.cu_host.data(), device, host.numel(), stream(c.device)));
+  c.a.cu_seqlens = device;
+  c.a.cu_seqlens_host = c.cu_host.data();
+}
 void la_args(LaCall& c, PyObject* const* o, double scale) {   // q, k, v, g, h0, cu_seqlens
   c.k = tensor(o[1], "k");
   c.v = tensor(o[2], "v");
@@ -148,19 +168,8 @@ void la_args(LaCall& c, PyObject* const* o, double scale) {   // q, k, v, g, h0,
   const int64_t B = c.q.size(0), T = c.q.size(1), Hqk = c.q.size(2), dk = c.q.size(3), Hv = c.v.size(2), dv = c.v.size(3);
   int64_t N = B;
   if (cu.defined()) {
-    if (cu.dim() != 1 || cu.numel() < 1) bad(PyExc_ValueError, "cu_seqlens must be [N + 1]");
-    c.cu_host = cu.detach().to(at::kCPU, at::kInt).contiguous();
-    N = c.cu_host.numel() - 1;
-    if (cu.is_cuda() && cu.scalar_type() == at::kInt && cu.get_device() == c.device) {
-      c.cu_dev = cu.contiguous();
-    } else {   // from pageable memory: staged before the copy returns
-      c.cu_dev = make({N + 1}, at::kInt, c.device);
-      if (cudaMemcpyAsync(c.cu_dev.data_ptr(), c.cu_host.data_ptr(), (size_t)(N + 1) * 4, cudaMemcpyHostToDevice,
-                          (cudaStream_t)stream(c.device)) != cudaSuccess)
-        bad(PyExc_RuntimeError, "cu_seqlens could not be copied to the device");
-    }
-    c.a.cu_seqlens = static_cast<const int32_t*>(c.cu_dev.data_ptr());
-    c.a.cu_seqlens_host = static_cast<const int32_t*>(c.cu_host.data_ptr());
+    offsets(c, cu);
+    N = (int64_t)c.cu_host.size() - 1;
   }
   const bool head = c.g.dim() == 1;
   c.a.q = is(c.q, at::kBFloat16, c.q.sizes(), c.device, "q");

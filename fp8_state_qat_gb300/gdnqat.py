@@ -34,7 +34,7 @@ EXPORTED = ("gdn_chunk_fwd_workspace_size", "gdn_chunk_fwd", "gdn_chunk_fwd_noal
             "gdn_prefill_decode_workspace_size", "gdn_prefill_decode_fwd",
             "gdn_chunk_bwd_workspace_size", "gdn_chunk_bwd", "kda_chunk_bwd_workspace_size", "kda_chunk_bwd",
             "kda_prefill_decode_workspace_size", "kda_prefill_decode_fwd",
-            "gdn_decode_step", "fp8_tile_qdq", "int8_block_qdq", "gdn_status_string", "gdn_check_device_status",
+            "gdn_decode_step", "fp8_tile_qdq", "int8_block_qdq", "gdn_status_string", "gdn_check_device_status", "gdn_upload_i32",
             "la_chunk_fwd_workspace_size", "la_chunk_bwd_workspace_size", "la_chunk_fwd", "la_chunk_bwd",
             "la_decode_step", "gated_norm_fwd", "gated_norm_bwd_workspace_size", "gated_norm_bwd",
             "residual_norm_fwd", "residual_norm_bwd_workspace_size", "residual_norm_bwd")
@@ -124,6 +124,7 @@ def load(build_if_missing: bool = True):
         for fn, res, args in (
                 ("la_chunk_fwd_workspace_size", SZ, [LA]), ("la_chunk_bwd_workspace_size", SZ, [LA]),
                 ("la_chunk_fwd", ctypes.c_int, [LA, P, SZ, P]), ("la_chunk_bwd", ctypes.c_int, [LA, LG, P, SZ, P]),
+                ("gdn_upload_i32", ctypes.c_int, [P, P, I64, P]),
                 ("la_decode_step", ctypes.c_int, [P] * 7 + [I32] * 5 + [F, U32, P]),
                 ("gated_norm_fwd", ctypes.c_int, [P, I32, P, P, I32, P, I64, I32, F, P]),
                 ("gated_norm_bwd_workspace_size", SZ, [I64, I32]),

@@ -17,7 +17,7 @@ from .gdnqat import LaArgs, _check, _state_flags, load
 
 LA_FLAG_HEAD_DECAY = 1
 _ENTRIES = ("la_chunk_fwd", "la_chunk_fwd_workspace_size", "la_chunk_bwd", "la_chunk_bwd_workspace_size",
-            "la_decode_step", "gated_norm_fwd", "gated_norm_bwd", "gated_norm_bwd_workspace_size", "residual_norm_fwd",
+            "gdn_upload_i32", "la_decode_step", "gated_norm_fwd", "gated_norm_bwd", "gated_norm_bwd_workspace_size", "residual_norm_fwd",
             "residual_norm_bwd", "residual_norm_bwd_workspace_size")
 
 
@@ -70,8 +70,9 @@ def la_chunk_fwd(q, k, v, g, h0=None, cu_seqlens=None, *, scale=1.0, o=None, hT=
                  workspace=None, stream=None):
     """Linear attention with a decay for each head: S_t = exp(g_t) S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t.
     q, k [B,T,Hqk,dk] bf16; v [B,T,Hv,dv] bf16 (value head h reads q/k head h // (Hv // Hqk)); g
-    [B,T,Hv] fp32, or [Hv] for one fixed decay per head; h0 [N,Hv,dk,dv] fp32 or None; cu_seqlens int32
-    [N+1] (CPU or CUDA) of sequences packed on the T axis of B = 1, or None. dk, dv in {64, 128}.
+    [B,T,Hv] fp32, or [Hv] for one fixed decay per head; h0 [N,Hv,dk,dv] fp32 or None; cu_seqlens [N+1] of
+    whole numbers of sequences packed on the T axis of B = 1, or None: read before the call returns, by waiting for
+    the stream where it is a CUDA tensor, which a captured call therefore refuses. dk, dv in {64, 128}.
     Returns (o [B,T,Hv,dv] bf16, hT [N,Hv,dk,dv] fp32 or None)."""
     if stream is None:
         r = _ext.la_chunk_fwd(q, k, v, g, h0, cu_seqlens, scale, o, hT, output_final_state, workspace)

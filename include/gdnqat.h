@@ -336,6 +336,11 @@ gdn_status residual_norm_bwd(const void* dx, const void* dh_out, const void* y, 
                              float* dw_post, float* dw_pre, int64_t rows, int32_t D, float alpha, float eps,
                              void* workspace, size_t workspace_bytes, gdn_stream_t stream);
 
+/* n int32 values from host memory to device memory, in stream order, carried by the launches' own parameters: the host
+ * memory is read before the call returns and may be reused or freed at once, pinned or not, and a captured call
+ * writes at every replay what it was given. For the offsets of packed sequences; 1000 values a launch. */
+gdn_status gdn_upload_i32(const int32_t* host, int32_t* device, int64_t n, gdn_stream_t stream);
+
 /* Static description of a status code. */
 const char* gdn_status_string(gdn_status status);
 

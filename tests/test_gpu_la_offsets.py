@@ -1,0 +1,92 @@
+"""The offsets of packed sequences: whatever the caller's tensor is and becomes, a call works on the values that it was
+given. Every packed case here is compared with the same call on a plain CPU tensor, bit for bit."""
+import itertools
+
+import pytest
+import torch
+
+import layer_reference as ref
+from test_gpu_la import TOL, cuda, inputs, run_bwd, run_fwd
+
+pytestmark = pytest.mark.gpu
+LENS = [70, 1, 300, 0, 129]
+OTHER = torch.tensor([0, 5, 6, 400, 400, 500])
+
+
+def on_gpu(x, gr):
+    return [cuda(x[n]) for n in ("q", "k", "v", "g", "h0")], cuda(gr["dout"]), cuda(gr["dhT"])
+
+
+def both(gdn, d, cu, dout, dhT):
+    return gdn.la_chunk_fwd(*d, cu) + gdn.la_chunk_bwd(*d, cu, dout, dhT)
+
+
+@pytest.fixture
+def case(gdn):
+    x, gr = inputs(1, 0, 2, 4, 64, 128, seed=31, lens=LENS)
+    d, dout, dhT = on_gpu(x, gr)
+    want = both(gdn, d, x["cu"], dout, dhT)
+    torch.cuda.synchronize()
+    return x["cu"], d, dout, dhT, want
+
+
+def same(got, want):
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_pinned_and_rewritten_after_the_call(gdn, case, dtype):
+    cu, d, dout, dhT, want = case
+    pinned = cu.to(dtype).pin_memory()
+    torch.cuda._sleep(20_000_000)   # the stream is busy for some 10 ms while the host goes on
+    got = both(gdn, d, pinned, dout, dhT)
+    pinned.copy_(OTHER)
+    same(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_captured_and_rewritten_before_the_replay(gdn, case, dtype):
+    cu, d, dout, dhT, want = case
+    given = cu.to(dtype)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(gdn, d, given, dout, dhT)
+    given.copy_(OTHER)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        same(got, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64])
+def test_on_the_device(gdn, case, dtype):
+    cu, d, dout, dhT, want = case
+    given = cu.cuda().to(dtype)
+    got = both(gdn, d, given, dout, dhT)
+    given.copy_(OTHER)
+    same(got, want)
+    strided = torch.stack([given, given], 1)
+    strided[:, 0] = cu.cuda()
+    same(both(gdn, d, strided[:, 0], dout, dhT), want)
+
+
+def test_device_tensor_is_refused_in_a_capture(gdn, case):
+    cu, d, dout, dhT, want = case
+    given = cu.cuda()
+    with pytest.raises(ValueError, match="captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            gdn.la_chunk_fwd(*d, given)
+    same(both(gdn, d, cu, dout, dhT), want)
+
+
+def test_more_sequences_than_a_launch_carries(gdn):
+    lens = [n % 3 for n in range(2300)]
+    x, gr = inputs(1, 0, 1, 1, 64, 64, seed=32, lens=lens)
+    assert x["cu"].tolist() == [0, *itertools.accumulate(lens)]
+    o, hT = run_fwd(gdn, x, 1.0)
+    got = dict(o=o, hT=hT, **run_bwd(gdn, x, gr, 1.0))
+    want = ref.la(*(x[n] for n in ("q", "k", "v", "g", "h0", "cu")), 1.0, gr["dout"], gr["dhT"])
+    for n in want:
+        assert ref.rel(got[n], want[n]) <= TOL[n], n
