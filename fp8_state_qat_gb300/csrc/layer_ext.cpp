@@ -144,6 +144,8 @@ struct LaCall {
 // whatever becomes of the tensor after the call.
 void offsets(LaCall& c, const Tensor& cu) {
   if (cu.dim() != 1 || cu.numel() < 1) bad(PyExc_ValueError, "cu_seqlens must be [N + 1]");
+  if (!at::isIntegralType(cu.scalar_type(), false))
+    bad(PyExc_ValueError, "cu_seqlens must hold whole numbers, got %s", text(cu.scalar_type()));
   cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
   if (cu.is_cuda() && cudaStreamIsCapturing((cudaStream_t)stream(c.device), &capture) == cudaSuccess &&
       capture != cudaStreamCaptureStatusNone)
@@ -151,7 +153,10 @@ void offsets(LaCall& c, const Tensor& cu) {
   const Tensor host = cu.detach().to(at::kCPU, at::kLong).contiguous();
   const int64_t* x = static_cast<const int64_t*>(host.data_ptr());
   c.cu_host.resize((size_t)host.numel());
-  for (size_t i = 0; i < c.cu_host.size(); ++i) c.cu_host[i] = (int32_t)x[i];
+  for (size_t i = 0; i < c.cu_host.size(); ++i) {
+    if (x[i] != (int32_t)x[i]) bad(PyExc_ValueError, "cu_seqlens[%zu] does not fit in 32 bits", i);
+    c.cu_host[i] = (int32_t)x[i];
+  }
   c.cu_dev = make({host.numel()}, at::kInt, c.device);
   int32_t* const device = static_cast<int32_t*>(c.cu_dev.data_ptr());
   done("gdn_upload_i32", p_gdn_upload_i32(c.cu_host.data(), device, host.numel(), stream(c.device)));

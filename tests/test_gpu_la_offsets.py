@@ -81,6 +81,14 @@ def test_device_tensor_is_refused_in_a_capture(gdn, case):
     same(both(gdn, d, cu, dout, dhT), want)
 
 
+def test_values_that_do_not_fit(gdn, case):
+    cu, d, *_ = case
+    for bad, match in ((cu.long() + torch.tensor([0, 0, 0, 0, 0, 1 << 32]), "32 bits"), (cu.float(), "whole numbers"),
+                       (cu.view(1, -1), "N . 1")):
+        with pytest.raises(ValueError, match=match):
+            gdn.la_chunk_fwd(*d, bad)
+
+
 def test_more_sequences_than_a_launch_carries(gdn):
     lens = [n % 3 for n in range(2300)]
     x, gr = inputs(1, 0, 1, 1, 64, 64, seed=32, lens=lens)
