@@ -140,6 +140,12 @@ struct LaCall {
   std::vector<int32_t> cu_host;
   int device;
 };
+// Other Python threads run in its scope.
+struct NoGil {
+  PyThreadState* const state = PyEval_SaveThread();
+  ~NoGil() { PyEval_RestoreThread(state); }
+};
+
 // The offsets of packed sequences, read once: the host's validation and sizes and the kernels go by the same values,
 // whatever becomes of the tensor after the call.
 void offsets(LaCall& c, const Tensor& cu) {
@@ -150,7 +156,11 @@ void offsets(LaCall& c, const Tensor& cu) {
   if (cu.is_cuda() && cudaStreamIsCapturing((cudaStream_t)stream(c.device), &capture) == cudaSuccess &&
       capture != cudaStreamCaptureStatusNone)
     bad(PyExc_ValueError, "cu_seqlens on the device cannot be read while a graph is captured: pass a CPU tensor");
-  const Tensor host = cu.detach().to(at::kCPU, at::kLong).contiguous();
+  Tensor host;
+  {
+    NoGil others;   // from a CUDA tensor this waits for the stream, whose work may itself wait for another thread
+    host = cu.detach().to(at::kCPU, at::kLong).contiguous();
+  }
   const int64_t* x = static_cast<const int64_t*>(host.data_ptr());
   c.cu_host.resize((size_t)host.numel());
   for (size_t i = 0; i < c.cu_host.size(); ++i) {

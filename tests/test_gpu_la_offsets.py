@@ -1,6 +1,8 @@
 """The offsets of packed sequences: whatever the caller's tensor is and becomes, a call works on the values that it was
 given. Every packed case here is compared with the same call on a plain CPU tensor, bit for bit."""
 import itertools
+import threading
+import time
 
 import pytest
 import torch
@@ -70,6 +72,29 @@ def test_on_the_device(gdn, case, dtype):
     strided = torch.stack([given, given], 1)
     strided[:, 0] = cu.cuda()
     same(both(gdn, d, strided[:, 0], dout, dhT), want)
+
+
+def test_other_threads_run_while_a_call_waits(gdn, case):
+    cu, d, dout, dhT, want = case
+    given, ticks, stop = cu.cuda(), [0], threading.Event()
+
+    def count():
+        while not stop.is_set():
+            ticks[0] += 1
+            time.sleep(1e-3)
+    torch.cuda.synchronize()
+    t = threading.Thread(target=count)
+    t.start()
+    try:
+        torch.cuda._sleep(200_000_000)   # some 100 ms, which the call has to wait for
+        before = ticks[0]
+        o, hT = gdn.la_chunk_fwd(*d, given)
+        during = ticks[0] - before
+    finally:
+        stop.set()
+        t.join()
+    assert during >= 10
+    same((o, hT), want)
 
 
 def test_device_tensor_is_refused_in_a_capture(gdn, case):
