@@ -424,7 +424,8 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
         s[6] = fmaf(dhv[e], u, s[6]);
       }
       RowSum<TPR, 7>::run(s, sm, slot);
-      ry = rsqrtf(fmaf(s[0], inv_d, eps));
+      // rows past the end, all zero, add to the weights' gradients too: without a factor of 1 / sqrt(0 + 0)
+      ry = live ? rsqrtf(fmaf(s[0], inv_d, eps)) : 0.f;
       const float a = alpha * ry;
       ss = fmaf(a, fmaf(a, s[3], 2.f * s[2]), s[1]);
       sp = fmaf(a, s[5], s[4]);
@@ -461,7 +462,7 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
       ss = s[0];
       sp = s[1];
     }
-    const float rh = rsqrtf(fmaf(ss, inv_d, eps));
+    const float rh = live ? rsqrtf(fmaf(ss, inv_d, eps)) : 0.f;
     const float c = sp * inv_d * rh * rh;
 #pragma unroll
     for (int e = 0; e < E; ++e) {
