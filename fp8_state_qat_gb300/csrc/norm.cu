@@ -432,12 +432,12 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
       su = fmaf(a, s[3], s[2]);
       gu = s[6];
       pu = s[5];
-      // where h and a u nearly cancel, h' h' is summed from h' itself: decided alike by all who share a reduction
-      bool small = !(ss >= 0.1f * fmaf(a * a, s[3], s[1])) && live;
-      if (TPR <= 32) small = __any_sync(0xffffffffu, small);
+      // where h and a u nearly cancel, h' h' is summed from h' itself. The rows of a warp sum together, and each
+      // takes the sums if it is one of those, so that no row's result depends on its neighbours
+      const bool small = !(ss >= 0.1f * fmaf(a * a, s[3], s[1])) && live;
 #pragma unroll
       for (int e = 0; e < E; ++e) hv[e] = fmaf(a, yv[e] * w2[e], hv[e]);
-      if (small) {
+      if (TPR <= 32 ? __any_sync(0xffffffffu, small) : small) {
         float x[3] = {};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -446,9 +446,11 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
           x[2] = fmaf(hv[e], yv[e] * w2[e], x[2]);
         }
         RowSum<TPR, 3>::run(x, sm, slot);
-        ss = x[0];
-        sp = x[1];
-        su = x[2];
+        if (small) {
+          ss = x[0];
+          sp = x[1];
+          su = x[2];
+        }
       }
     } else {
       float s[2] = {0.f, 0.f};

@@ -44,3 +44,18 @@ def test_gated_norm_without_eps(gdn, R, D):
     for a, b, tol in zip((gdn.gated_norm_fwd(*d, eps=0.0), *gdn.gated_norm_bwd(cuda(dy), *d, eps=0.0)), want,
                          (None, None, None, TOL_W)):
         near(a, b, tol)
+
+
+@pytest.mark.parametrize("th", [BF, F32])
+@pytest.mark.parametrize("D", [40, 64, 128, 200, 512])
+def test_rows_do_not_depend_on_their_neighbours(gdn, D, th):
+    """A row whose h cancels alpha n takes its sums another way; the rows beside it keep every bit of theirs."""
+    R = 512
+    y, h, w1, w2, dx, dh = residual_case(R, D, th, True)
+    other = h.clone()
+    n = ref.residual_norm(y, torch.zeros(R, D), w1, w2, 0.5, 1e-6)[0]
+    other[::4] = (-n[::4]).to(th)
+    a, b = (gdn.residual_norm_bwd(*(cuda(t) for t in (dx, dh, y, s, w1, w2)), alpha=0.5)[:2] for s in (h, other))
+    keep = [r for r in range(R) if r % 4]
+    for s, t in zip(a, b):
+        assert torch.equal(s[keep], t[keep])
