@@ -170,12 +170,13 @@ __global__ void __launch_bounds__(256) la_group_sum_kernel(const float* x0, cons
 
 size_t up(size_t x) { return (x + 255) & ~(size_t)255; }
 
+// By sizes alone, so that a workspace serves every packing of the same sizes.
 struct Layout {
   size_t S, dS, tot, dec, rq, rk, aq, bk, edge, pq, pk, item, total;
 };
 Layout layout_of(const LaProblem& p, bool bwd) {
   const size_t items = (size_t)la_slots(p) * p.Hv, elems = (size_t)p.dk * p.dv, th = (size_t)p.B * p.T * p.Hv;
-  const int nseg = state_segments(p);
+  const int nseg = most_segments(p);
   Layout l{};
   size_t at = kStatusBytes;
   auto take = [&](size_t n) {
@@ -194,7 +195,7 @@ Layout layout_of(const LaProblem& p, bool bwd) {
     l.rk = take(th * 8);
     l.aq = take(th * 4);
     l.bk = take(th * 4);
-    if (!walks_beside(p)) l.edge = take(items * edge_parts(p) * 4);
+    if (nseg > 1 || !walks_beside(p)) l.edge = take(items * edge_parts(p) * 4);
     if (p.Hv != p.Hqk) {
       l.pq = take(th * p.dk * 4);
       l.pk = take(th * p.dk * 4);

@@ -212,6 +212,7 @@ struct StateRun {
 };
 int edge_parts(const LaProblem& p);
 int state_segments(const LaProblem& p);
+int most_segments(const LaProblem& p);   // of any packing of these sizes
 bool walks_beside(const LaProblem& p);
 // dependent: the launch before it in the stream is one of these kernels
 cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bool dependent, cudaStream_t stream);

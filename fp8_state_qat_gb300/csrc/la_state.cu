@@ -460,17 +460,21 @@ int64_t la_slots(const LaProblem& p) { return (int64_t)p.B * p.T / kC + p.N; }
 // segments 243 -> 207 us; 60 walks, 2 segments 260 -> 267 us; T 4096, 8 walks, 8 segments 52 -> 34 us; 50
 // walks, 3 segments 69 -> 69 us; T 1024, 2 segments 25 -> 32 us. So a walk is split into three segments or more
 // or not at all, and a segment keeps at least 4 chunks.
-int state_segments(const LaProblem& p) {
+static int segments_of(const LaProblem& p, int64_t longest) {
   const int64_t walks = (int64_t)p.N * p.Hv * (p.dv / kNV);
   if (walks == 0 || walks > kSMs / 3) return 1;
+  const int64_t chunks = (longest + kC - 1) / kC, most = std::min<int64_t>(kSMs / walks, chunks / 4);
+  return most >= 3 ? (int)most : 1;
+}
+int state_segments(const LaProblem& p) {
   int64_t longest = p.T;
   if (p.cu_host) {
     longest = 0;
     for (int n = 0; n < p.N; ++n) longest = std::max<int64_t>(longest, p.cu_host[n + 1] - p.cu_host[n]);
   }
-  const int64_t chunks = (longest + kC - 1) / kC, most = std::min<int64_t>(kSMs / walks, chunks / 4);
-  return most >= 3 ? (int)most : 1;
+  return segments_of(p, longest);
 }
+int most_segments(const LaProblem& p) { return segments_of(p, p.T); }
 
 // Few walks leave room for the backwards walk beside the forwards one: it then starts with it, and <S, dS>, which
 // it would take from the stored S on its way, is left to the dg kernel. A training step at 5 packed sequences of 1 to

@@ -52,7 +52,8 @@ def _elsewhere(fn, t, stream, *args, **kw):
 
 def la_chunk_workspace_bytes(q_shape, v_shape, cu_seqlens=None, *, head_decay=False, backward=False):
     """la_chunk_fwd_workspace_size (backward: la_chunk_bwd_workspace_size) for q [B,T,Hqk,dk] and v
-    [B,T,Hv,dv] (shapes only); 0 for shapes that the calls refuse."""
+    [B,T,Hv,dv] (shapes only; of cu_seqlens only the number of sequences matters); 0 for shapes that the calls
+    refuse."""
     B, T, Hqk, dk = q_shape
     Hv, dv = v_shape[2], v_shape[3]
     cu_host, N = None, B

@@ -289,7 +289,8 @@ typedef struct {
 } la_chunk_grads;
 
 /* Device workspace of la_chunk_fwd / la_chunk_bwd in bytes; 0 for invalid arguments. Depends on
- * sizes and flags only. Contents need no initialization. */
+ * sizes and flags only: one workspace serves every packing of T tokens into N sequences. Contents need no
+ * initialization. */
 size_t la_chunk_fwd_workspace_size(const la_chunk_args* args);
 size_t la_chunk_bwd_workspace_size(const la_chunk_args* args);
 /* o for every token and (hT) the final state of every sequence; empty sequences give hT = h0.
