@@ -57,7 +57,7 @@ def _ext_deps():
 
 
 def up_to_date() -> bool:
-    return newer_than(LIB_PATH, _deps()) and newer_than(EXT_PATH, _ext_deps())
+    return newer_than(LIB_PATH, _deps())
 
 
 def compile_extension(out: str = EXT_PATH) -> str:
@@ -116,17 +116,27 @@ def compile_library(sources, out: str, obj_dir: str, verbose: bool = False) -> s
     return out
 
 
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile csrc/*.cu into libgdnqat.so (skipped when it is up to date)."""
+    if not force and up_to_date():
+        return LIB_PATH
+    return compile_library(_sources(), LIB_PATH, OBJ_DIR, verbose=verbose)
+
+
+def build_extension(force: bool = False) -> str:
+    """Compile csrc/layer_ext.cpp into gdnqat_layer.so (skipped when it is up to date). Only the operators of
+    layer.py need it."""
+    if not force and newer_than(EXT_PATH, _ext_deps()):
+        return EXT_PATH
+    return compile_extension(EXT_PATH)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile csrc/*.cu into libgdnqat.so and csrc/layer_ext.cpp into gdnqat_layer.so, side by side (each
-    skipped when it is up to date)."""
+    """The library and the extension, side by side."""
     with ThreadPoolExecutor(max_workers=1) as ex:
-        ext = None
-        if force or not newer_than(EXT_PATH, _ext_deps()):
-            ext = ex.submit(compile_extension)
-        if force or not newer_than(LIB_PATH, _deps()):
-            compile_library(_sources(), LIB_PATH, OBJ_DIR, verbose=verbose)
-        if ext is not None:
-            ext.result()
+        ext = ex.submit(build_extension, force)
+        build_library(force, verbose)
+        ext.result()
     return LIB_PATH
 
 

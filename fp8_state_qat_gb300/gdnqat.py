@@ -92,7 +92,7 @@ def load(build_if_missing: bool = True):
         if not os.path.exists(_build.LIB_PATH) or (build_if_missing and not _build.up_to_date()):
             if not build_if_missing:
                 raise RuntimeError(f"CUDA library not built: {_build.LIB_PATH}")
-            _build.build()
+            _build.build_library()
         lib = ctypes.CDLL(_build.LIB_PATH)
         P, I32, U32, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_float
         for fn in ("gdn_chunk_fwd_workspace_size", "kda_chunk_fwd_workspace_size",

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import threading
 
 import torch
 
@@ -21,18 +22,23 @@ _ENTRIES = ("la_chunk_fwd", "la_chunk_fwd_workspace_size", "la_chunk_bwd", "la_c
             "residual_norm_bwd", "residual_norm_bwd_workspace_size")
 
 
+_lock = threading.Lock()
+
+
 class _Unloaded:
-    """Stands for the extension until its first use, which loads it and the library."""
+    """Stands for the extension until its first use, which loads it and the library (building what is missing)."""
 
     def __getattr__(self, name):
         global _ext
         lib = load()
-        spec = importlib.util.spec_from_file_location("gdnqat_layer", _build.EXT_PATH)
-        ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(ext)
-        ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, _check)
-        _ext = ext
-        return getattr(ext, name)
+        with _lock:
+            if _ext is self:
+                spec = importlib.util.spec_from_file_location("gdnqat_layer", _build.build_extension())
+                ext = importlib.util.module_from_spec(spec)
+                spec.loader.exec_module(ext)
+                ext.bind({n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _ENTRIES}, _check)
+                _ext = ext
+        return getattr(_ext, name)
 
 
 _ext = _Unloaded()
