@@ -49,6 +49,8 @@ def _elsewhere(fn, t, stream, *args, **kw):
     allocations belong to that stream too."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
     with torch.cuda.device(t.device):
         if stream is None:
             return fn(*args, **kw)
