@@ -490,8 +490,8 @@ residual_norm_bwd_kernel(const __nv_bfloat16* __restrict__ dx, const H* dh_out,
   write_partials<TPR, VEC, 2>(acc, red, out, D);
 }
 
-// out[m][d] = the sum of the m-th array's `parts` partial rows, in a fixed order: 8 lanes of rows per
-// column, each summing every 8th row, added by an xor tree.
+// out[m][d] = the sum of the m-th array's `parts` partial rows, in a fixed order: 32 threads a column, each
+// summing every 32nd row, and their sums added through shared memory by one thread, in four running sums.
 __global__ void __launch_bounds__(256) sum_partials_kernel(const float* __restrict__ p0, const float* __restrict__ p1,
                                                            float* __restrict__ o0, float* __restrict__ o1, int parts,
                                                            int D) {

@@ -1,5 +1,7 @@
 """Rows of the norms that share a CTA: those past the end, and neighbours. References and tolerances as in
 test_gpu_norm.py."""
+import ctypes
+
 import pytest
 import torch
 
@@ -59,3 +61,24 @@ def test_rows_do_not_depend_on_their_neighbours(gdn, D, th):
     keep = [r for r in range(R) if r % 4]
     for s, t in zip(a, b):
         assert torch.equal(s[keep], t[keep])
+
+
+@pytest.mark.parametrize("post", [False, True])
+@pytest.mark.parametrize("th", [BF, F32])
+@pytest.mark.parametrize("D", [100, 256, 2048, 8192])
+def test_gradient_of_the_stream_in_place(gdn, D, th, post):
+    """dh may be dh_out (the C call; the Python one makes its outputs): the same bits as in separate buffers."""
+    R = 37
+    y, h, w1, w2, dx, dh = (cuda(t) for t in residual_case(R, D, th, post))
+    want = gdn.residual_norm_bwd(dx, dh, y, h, w1, w2, alpha=0.5)
+    lib = gdn.load()
+    dy, dw1, dw2 = torch.empty_like(y), torch.empty(D, device="cuda"), torch.empty(D, device="cuda") if post else None
+    n = lib.residual_norm_bwd_workspace_size(R, D)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    P = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    bf16, f32 = 0, 1
+    status = lib.residual_norm_bwd(P(dx), P(dh), P(y), P(h), f32 if th == F32 else bf16, P(w2), P(w1), f32, P(dy), P(dh),
+                                   P(dw2), P(dw1), R, D, 0.5, 1e-6, P(ws), n, torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    for a, b in zip((dy, dh, dw1, dw2), want):
+        assert a is b is None or torch.equal(a, b)
