@@ -9,7 +9,9 @@
 // (two INT8 blocks wide), so a CTA never waits for another, and few sequences still spread over
 // dv / 64 times as many SMs. Warp w owns 16 columns; lane 4 rg + cg holds rows rg, rg + 8, ... of
 // four columns in 16-byte accesses, and the sums over rows are xor shuffles in a fixed order. 512 sequences, 32
-// heads, d 128, E4M3: 341 us, 6.34 TB/s (0.95 of the measured copy bandwidth); one sequence, 16 heads: 4.7 us a call.
+// heads, d 128, E4M3: 342 us, 6.32 TB/s (0.95 of the measured copy bandwidth); INT8: 449 us, 4.8 TB/s: a scale and
+// a reciprocal a row lengthen the chain between a CTA's loads and stores, and four CTAs an SM do not cover it (issue
+// slots 35 % used); one sequence, 16 heads: 5 us a call.
 // The scale is amax times the rounded constant 1 / 448 (1 / 127), one multiply and at most an ulp from
 // the quotient, 1 for an all-zero tile; the code is that of the correctly rounded quotient x / s, by paired fused
 // multiply-adds (an IEEE divide an element took 425 us).

@@ -15,9 +15,12 @@
 // rounding, and e_t . (a_t^T St) with the state in two bf16 terms.
 //
 // The weighted scores and the states are each a sum of two bf16 terms (16 bits and a sign: 2^-18 of the value), so
-// that the outputs' own rounding to bf16 is the only one that shows: o, dq, dk, dv are off by 1.7e-3 of 64 bits, as
-// their rounded values are; with one term of each it was 2.3e-3. dg is fp32 and rests on the same two-term states:
-// they leave it 1e-6 to 3e-6 off where the states carry much of it. A third term would be 32 KB more a chunk and state.
+// that the outputs' own rounding to bf16 is the only one that shows: o, dq, dk, dv are off by 1.7e-3 of 64 bits, as the
+// rounded 64-bit result is; with one term of each it was 2.3e-3, in 55 instead of 65 us (o) and 162 instead of 185 (dq,
+// dk, dv) at the size below. dg is fp32 and rests on the same states: 4e-7 to 3e-6 off, up to 6e-6 in sequences of a few
+// tokens whose gradient is all of the given states'. A third term would bring that to 3e-7: 32 KB more a chunk and state
+// here, and in the walk room for one set of V's terms instead of two, which alone costs 10 us a walk there (8 % of a
+// training step in all).
 //
 // What bounds it is the traffic: 3 or 4 token tiles and 2 or 4 state terms in (32 KB each at d = 128), one tile out a
 // role. So one persistent CTA per SM keeps six 32 KB tiles filled ahead by TMA, across items; the three roles of a
@@ -26,8 +29,8 @@
 // loop bodies are kept small and shared by all roles: unrolled per block and role, the code outgrew the instruction cache
 // and the same work took 4 (o) to 10 times (gradients) as long.
 //
-// At 4 x 4096 tokens, 16 heads, d 128: o 55 us, 338 MB of tiles, 6.2 TB/s (0.92 of the measured copy bandwidth); dq, dk, dv
-// 162 us, 743 MB, 4.6 TB/s: all four token tiles of a chunk are in use until its last role, and the next chunk's
+// At 4 x 4096 tokens, 16 heads, d 128 (cold): o 65 us, 405 MB of tiles, 6.2 TB/s (0.93 of the measured copy bandwidth); dq, dk,
+// dv 185 us, 743 MB, 4.0 TB/s: all four token tiles of a chunk are in use until its last role, and the next chunk's
 // arrive 3 us after they fall free.
 #include <algorithm>
 #include <cstddef>

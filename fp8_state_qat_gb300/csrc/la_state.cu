@@ -18,9 +18,10 @@
 // contribution from a zero state, a scan joins them, and the second launch walks all segments at once
 // from their true starting states.
 //
-// At 4 x 4096 tokens, 16 heads, d 128 (128 CTAs of 32 steps): forwards 48 us, backwards 53 us (two-term S) and 74 us
-// (dS, with S read again for <S, dS>). Bound by tile traffic: 48 KB in and 16 to 64 KB out or in again a step, K by both
-// value tiles' CTAs, 5.6 to 6.5 TB/s from L2; a step takes 2.4 k cycles, its products 1.0 k, its conversion 1.4 k.
+// At 4 x 4096 tokens, 16 heads, d 128 (128 CTAs of 32 steps, cold): S 55 us, dS 76 us (with S read again for <S, dS>).
+// Bound by the length of a step, a chain of hand-overs: 2.4 k cycles, of which the products take 1.0 k and V's
+// conversion 1.4 k side by side. Not by traffic (48 KB in and 32 to 64 KB out or in again a step, 4 to 5 TB/s of DRAM): with K sent
+// once to both value tiles' CTAs, a third of the loads less, it took longer, each step waiting for the slower of the two.
 #include <algorithm>
 
 #include "la_chunk.cuh"
@@ -456,9 +457,9 @@ constexpr int kSMs = 152;
 int64_t la_slots(const LaProblem& p) { return (int64_t)p.B * p.T / kC + p.N; }
 
 // One CTA of a walk runs per SM, and a split walk takes two passes over K and V and a join. Forward at one
-// sequence, d 128, whole walks against split ones: T 16384, 16 walks, 9 segments 190 -> 82 us; 50 walks, 3
-// segments 243 -> 207 us; 60 walks, 2 segments 260 -> 267 us; T 4096, 8 walks, 8 segments 52 -> 34 us; 50
-// walks, 3 segments 69 -> 69 us; T 1024, 2 segments 25 -> 32 us. So a walk is split into three segments or more
+// sequence, d 128, whole walks against split ones: T 16384, 16 walks, 9 segments 211 -> 91 us; 50 walks, 3
+// segments 276 -> 236 us; 60 walks, 2 segments 295 -> 305 us; T 4096, 8 walks, 8 segments 56 -> 35 us; 50
+// walks, 3 segments 83 -> 77 us; T 1024, 8 walks, 2 segments 26 -> 33 us. So a walk is split into three segments or more
 // or not at all, and a segment keeps at least 4 chunks.
 static int segments_of(const LaProblem& p, int64_t longest) {
   const int64_t walks = (int64_t)p.N * p.Hv * (p.dv / kNV);
@@ -478,8 +479,8 @@ int most_segments(const LaProblem& p) { return segments_of(p, p.T); }
 
 // Few walks leave room for the backwards walk beside the forwards one: it then starts with it, and <S, dS>, which
 // it would take from the stored S on its way, is left to the dg kernel. A training step at 5 packed sequences of 1 to
-// 1000 tokens, 4 heads (40 CTAs): 79 -> 68 us; 3 x 1000 tokens, 8 heads, d 64 (24): 87 -> 74; 2 x 2048, 18 heads, d 128
-// (72): 177 -> 175; at 4 x 1024, 16 heads (128, of which 24 find a free SM): 143 -> 168, so only where all have one.
+// 1000 tokens, 4 heads (40 CTAs): 82 -> 75 us; 3 x 1000 tokens, 8 heads, d 64 (24): 89 -> 78; 2 x 2048, 18 heads, d 128
+// (72): 181 -> 180; at 4 x 1024, 16 heads (128, of which 24 find a free SM): 144 -> 171, so only where all have one.
 bool walks_beside(const LaProblem& p) {
   return state_segments(p) == 1 && 2 * (int64_t)p.N * p.Hv * (p.dv / kNV) <= kSMs;
 }
@@ -505,8 +506,9 @@ cudaError_t launch_states(const LaProblem& p, const StateRun& r, int* status, bo
   Params s{{p.cu, p.T, p.N}, {p.g, p.Hv, p.head_decay}, r.s0, r.sT, r.seg_tot, r.seg_dec, r.edge,
            status, p.Hqk, p.dk, p.dv, r.reverse, state_segments(p), 0, r.states != nullptr, r.other != nullptr,
            r.other ? 1 : 2, r.scale, r.beside};
-  // Walks of unequal lengths: the longest first, so that the last ones to start are short (b = 1, 8 packed
-  // sequences of 1 to 8192 tokens, 32 heads: an eighth of the time). Many sequences even out by themselves.
+  // Walks of unequal lengths: the longest first, so that the last ones to start are short (63 sequences of 128 tokens and
+  // one of 16384 that comes last, 16 heads: 286 us, in the caller's order 367). The order of up to 64 fits the
+  // launch's parameters; from 65 on it is the caller's, and a long one that comes last runs alone.
   if (p.cu_host && p.N <= 64) {
     s.sorted = 1;
     for (int i = 0; i < p.N; ++i) s.order[i] = (uint8_t)i;
