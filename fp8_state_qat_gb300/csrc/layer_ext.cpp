@@ -7,6 +7,7 @@
 
 #include <cstdarg>
 #include <initializer_list>
+#include <optional>
 #include <string>
 #include <vector>
 
@@ -158,7 +159,10 @@ void offsets(LaCall& c, const Tensor& cu) {
     bad(PyExc_ValueError, "cu_seqlens on the device cannot be read while a graph is captured: pass a CPU tensor");
   Tensor host;
   {
-    NoGil others;   // from a CUDA tensor this waits for the stream, whose work may itself wait for another thread
+    // From a CUDA tensor this waits for the stream, whose work may itself wait for another thread. A CPU tensor's values
+    // are there: to give the lock away for them could cost the time that a busy thread keeps it, milliseconds.
+    std::optional<NoGil> others;
+    if (cu.is_cuda()) others.emplace();
     host = cu.detach().to(at::kCPU, at::kLong).contiguous();
   }
   const int64_t* x = static_cast<const int64_t*>(host.data_ptr());
